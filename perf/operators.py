@@ -322,7 +322,7 @@ def _own(s):
         kvc.check(kvc.kvc_pages_reserve(h, s["table"], s["refs"], s["n"], s["grown"], ws, ws.numel(), stream), "kvc_pages_reserve")
         return s["table"], s["refs"], s["K"], s["V"]
     kvc.check(kvc.kvc_pages_free(h, s["table"], s["refs"], s["kept"], stream), "kvc_pages_free")
-    kvc.check(kvc.kvc_pages_compact(h, s["table"], s["refs"], s["live"], ws, ws.numel(), stream), "kvc_pages_compact")
+    kvc.check(kvc.kvc_pages_compact(h, s["table"], s["refs"], None, s["live"], ws, ws.numel(), stream), "kvc_pages_compact")
     return s["table"], s["refs"], s["live"], s["K"], s["V"]
 
 
