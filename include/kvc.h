@@ -330,6 +330,220 @@ kvc_status kvc_prefill_attn(kvc_cache *h, int32_t layer, const void *q,
                             const int32_t *cache_index, int32_t T_new,
                             void *out, void *stream);
 
+/* ---- prompts and drafted trees ------------------------------------------- */
+
+/* The calls of this section take new tokens whose K and V rows are not in the
+ * cache yet, several per sequence, and attend them over the sequence's cached
+ * rows and over one another; two further calls then store those rows.  They
+ * work on contiguous and on paged handles (the pages' rows are read and
+ * written through the block table).
+ *
+ * kvc_prompt_attn and kvc_tree_attn take KVC_BF16, KVC_FP16 and KVC_FP32
+ * caches of every head width and head group kvc_check_config accepts
+ * (KVC_ERR_UNSUPPORTED for KVC_INT8).  Arithmetic: fp32 products and
+ * accumulation (of operands in the cache's type; softmax probabilities are
+ * rounded to a 16-bit cache's type before they meet V), one
+ * round-to-nearest-even at the end.  A 16-bit cache with d_head 64 or 128 runs
+ * on the tensor cores, the others on the CUDA cores.
+ *
+ * Rows that a query does not see never reach its output, whatever finite
+ * values they hold; cached rows at or past cache_index[b], and new rows past
+ * the sequence's own, may hold anything.
+ * (An infinity or NaN in a V row that one token of a sequence sees may reach
+ * the other tokens of the same sequence and KV head.)
+ *
+ * The workspace of these calls (kvc_rows_workspace_bytes, 256-byte aligned)
+ * need not be initialised and keeps nothing between calls; it may serve any
+ * number of handles and captured graphs whose launches are ordered, but not
+ * two calls that overlap on the GPU.  All of them: the handle's device has to be current
+ * (KVC_ERR_INVALID otherwise). */
+
+/* Bytes of workspace for one kvc_prompt_attn or kvc_tree_attn call: the
+ * partial results (max, sum, accumulator) of sequences split over several
+ * CTAs.  0 if cfg is invalid. */
+uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
+
+/* Causal attention of whole prompts of different lengths, packed one behind
+ * the other ("KV-Cache Mechanics", AR Static KV-Cache: prefill; "10.3",
+ * section 7, prefix caching: a cached prefix shared by later requests).  Token
+ * i of sequence b (packed row r = cu_seqlens[b] + i) attends over the
+ * sequence's cached rows j < cache_index[b] and over its packed rows
+ * cu_seqlens[b] .. r:
+ *   out[r, h, :] = softmax( q[r, h, :] . [K_l[b, h / g, :cache_index[b]]; k[cu_seqlens[b] : r + 1, h / g]]
+ *                           / sqrt(d_h) ) . [V_l[...]; v[...]]
+ * The rows are read from k and v; kvc_append_packed stores them into the cache
+ * (before or after).
+ *   layer        0 <= layer < n_layers (whose cached rows are read)
+ *   q            device, [total, H, d_h], 16-byte aligned
+ *   k, v         device, [total, H_kv, d_h], 16-byte aligned
+ *   cu_seqlens   device int32 [B + 1]: packed row at which each sequence
+ *                starts, and the end of the last; B = cfg.batch.  A sequence
+ *                without new tokens has cu_seqlens[b + 1] == cu_seqlens[b].  A
+ *                sequence whose range is reversed or leaves [0, total] is
+ *                skipped (its output rows are left unwritten) and
+ *                KVC_ERR_DEVICE_INDEX is recorded.  Packed rows outside every
+ *                sequence are left unwritten.
+ *   cache_index  device int32 [B]: cached rows of each sequence, or NULL: no
+ *                sequence has any.  Outside [0, max_context]: skipped and
+ *                recorded like a bad range.
+ *   total        packed rows, >= 0 (0: no-op)
+ *   workspace    device, ws_bytes >= kvc_rows_workspace_bytes(cfg)
+ *   out          device, [total, H, d_h], 16-byte aligned
+ * Paged handles: a block-table entry outside [0, num_blocks) among a
+ * sequence's cached rows records KVC_ERR_DEVICE_INDEX; that sequence's output
+ * is then undefined.
+ * Host errors: KVC_ERR_INVALID, KVC_ERR_UNSUPPORTED, KVC_ERR_ALIGNMENT,
+ * KVC_ERR_WORKSPACE, KVC_ERR_CUDA. */
+kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const void *k, const void *v,
+                           const int32_t *cu_seqlens, const int32_t *cache_index, int32_t total,
+                           void *workspace, uint64_t ws_bytes, void *out, void *stream);
+
+/* Store packed K and V rows into the cache: row i of sequence b goes to
+ * position cache_index[b] + i (position i when cache_index is NULL); the
+ * ragged counterpart of kvc_append, for every cache type (an int8 cache:
+ * k and v are bf16 and each row is quantised as it is written).
+ *   k, v, cu_seqlens, total   as for kvc_prompt_attn
+ *   cache_index  device int32 [B] or NULL.  A sequence whose rows would leave
+ *                [0, max_context) is skipped and KVC_ERR_DEVICE_INDEX recorded;
+ *                so is one with a bad range in cu_seqlens.  Paged handles: rows
+ *                whose table entry is outside [0, num_blocks) are not written
+ *                and KVC_ERR_DEVICE_INDEX is recorded.
+ * Host errors: KVC_ERR_INVALID, KVC_ERR_ALIGNMENT, KVC_ERR_CUDA. */
+kvc_status kvc_append_packed(kvc_cache *h, int32_t layer, const void *k, const void *v,
+                             const int32_t *cu_seqlens, const int32_t *cache_index, int32_t total,
+                             void *stream);
+
+/* Attention of a tree of T drafted tokens per sequence over the cache ("10.3",
+ * section 8, speculative decoding: several drafted tokens verified by one
+ * forward pass).  Drafted token t of sequence b attends over the cached rows
+ * j < cache_index[b] and over the drafted tokens s whose bit is set in its
+ * mask row -- with a tree, the tokens on its path from the root, itself
+ * included:
+ *   out[b, i, t, :] = softmax( q[b, i, t, :] . [K_l[b, i / g, :cache_index[b]]; k_new[b, i / g, s...]]
+ *                              / sqrt(d_h) ) . [V_l[...]; v_new[...]]
+ * Nothing is written to the cache; kvc_tree_commit stores the accepted path.
+ *   q             device, [B, H, T, d_h], 16-byte aligned
+ *   k_new, v_new  device, [B, H_kv, T, d_h], 16-byte aligned
+ *   cache_index   device int32 [B], in [0, max_context]; otherwise the sequence
+ *                 is skipped (output unwritten), KVC_ERR_DEVICE_INDEX recorded
+ *   n_nodes       device int32 [B]: drafted tokens of each sequence (the first
+ *                 n_nodes[b] of the T; rows behind them are neither attended
+ *                 nor written), or NULL: T everywhere.  Outside [0, T]: skipped
+ *                 and recorded
+ *   tree_mask     device uint32 [B, T, ceil(T / 32)]: bit s % 32 of word s / 32
+ *                 of row t: t attends to s.  Any mask is allowed; a token that
+ *                 sees no row at all gets zeros.  NULL: a chain (t attends to
+ *                 s <= t)
+ *   T             1 .. max_context
+ *   max_index_hint  host; 0, or an upper bound on cache_index used only to size
+ *                 the launch
+ *   workspace     device, ws_bytes >= kvc_rows_workspace_bytes(cfg)
+ *   out           device, [B, H, T, d_h], 16-byte aligned
+ * Paged handles and host errors as for kvc_prompt_attn. */
+kvc_status kvc_tree_attn(kvc_cache *h, int32_t layer, const void *q, const void *k_new,
+                         const void *v_new, const int32_t *cache_index, const int32_t *n_nodes,
+                         const uint32_t *tree_mask, int32_t T, int32_t max_index_hint,
+                         void *workspace, uint64_t ws_bytes, void *out, void *stream);
+
+/* Store an accepted path's K and V rows into the cache, for layers
+ * [layer, layer + n_layers) in one launch:
+ *   K_l[b, j, cache_index[b] + i, :] = k_new[l - layer, b, j, path[b, i], :]   for i < n_accept[b]
+ * and the same for V (an int8 cache: k_new / v_new are bf16, quantised as they
+ * are written).
+ *   k_new, v_new  device, [n_layers, B, H_kv, T, d_h], 16-byte aligned
+ *   cache_index   device int32 [B]
+ *   path          device int32 [B, P]: drafted tokens in [0, T)
+ *   n_accept      device int32 [B], in [0, P]
+ *   T, P          >= 1
+ * A sequence with a value out of range (a path entry below n_accept[b], or
+ * rows that would leave [0, max_context)) is skipped and KVC_ERR_DEVICE_INDEX
+ * recorded.  Paged handles as for kvc_append_packed.
+ * Host errors: KVC_ERR_INVALID, KVC_ERR_ALIGNMENT, KVC_ERR_CUDA. */
+kvc_status kvc_tree_commit(kvc_cache *h, int32_t layer, int32_t n_layers, const void *k_new,
+                           const void *v_new, const int32_t *cache_index, const int32_t *path,
+                           const int32_t *n_accept, int32_t T, int32_t P, void *stream);
+
+/* ---- pages of a paged cache ------------------------------------------------- */
+
+/* Forking, growing, freeing, copying and compacting the blocks ("pages") of a
+ * paged cache ("10.3", section 7: block tables; sequences that share a prefix
+ * share its blocks).  The state is the handle's block table and one int32
+ * reference count per physical block, both owned by the caller and changed in
+ * stream order by these calls; nothing else is kept.
+ *   block_table  device int32 [B, max_context / 16], the table the handle was
+ *                allocated with (KVC_ERR_INVALID otherwise).  An entry of -1
+ *                is "no block"; entries out of [-1, num_blocks) are treated
+ *                like -1 and KVC_ERR_DEVICE_INDEX is recorded
+ *   refcount     device int32 [num_blocks], 16-byte aligned: how many table entries name
+ *                each block (a caller may hold further references, to pin a
+ *                prefix for instance, by adding to a count).  A block whose
+ *                count is 0 is free
+ * A cache starts with a table of -1 and counts of 0.  A block may be named by
+ * several sequences, each at the same logical index.  Every result is
+ * defined exactly: it depends on the state and the arguments, never on timing.
+ * A sequence whose arguments are out of range keeps its pages and
+ * KVC_ERR_DEVICE_INDEX is recorded.  These calls need a paged handle
+ * (KVC_ERR_UNSUPPORTED otherwise) whose device is current, and at most 8192
+ * sequences.  Other host errors: KVC_ERR_INVALID,
+ * KVC_ERR_ALIGNMENT, KVC_ERR_WORKSPACE, KVC_ERR_CUDA. */
+
+/* Bytes of workspace of kvc_pages_reserve and kvc_pages_compact (16-byte
+ * aligned; not initialised, nothing kept between calls; not for two calls that
+ * overlap on the GPU).  0 for an invalid cfg or num_blocks <= 0. */
+uint64_t kvc_pages_workspace_bytes(const kvc_config *cfg, int32_t num_blocks);
+
+/* Sequence b takes over the pages of sequence parent[b], all at once:
+ * table[b, :] = (old table)[parent[b], :], counts follow.  parent[b] == b keeps
+ * a sequence, several b with one parent fork it (beams, parallel samples),
+ * -1 leaves b without pages.  No row is copied: shared pages are split by
+ * kvc_pages_reserve before they are written.
+ *   parent  device int32 [B], in [-1, B) */
+kvc_status kvc_pages_fork(kvc_cache *h, int32_t *block_table, int32_t *refcount,
+                          const int32_t *parent, void *stream);
+
+/* Make rows [len[b], new_len[b]) of every sequence writable: missing pages are
+ * added, and a page of that range that other sequences share is replaced by a
+ * page of b's own, with the rows below len[b] copied into it, every layer, K
+ * and V.  Of the sequences that share a page and reserve it in one call,
+ * the one with the highest index keeps it if nobody else holds it.  New pages
+ * are the lowest-numbered free blocks (free before the call), handed out in
+ * the order of (sequence, logical block).  If there are fewer free blocks than
+ * needed, nothing changes for any sequence and KVC_ERR_CAPACITY is recorded.
+ *   len, new_len  device int32 [B], 0 <= len[b] <= new_len[b] <= max_context
+ *                 (len[b] == new_len[b]: b is not touched); rows below len[b]
+ *                 have to have pages
+ *   workspace     device, ws_bytes >= kvc_pages_workspace_bytes */
+kvc_status kvc_pages_reserve(kvc_cache *h, int32_t *block_table, int32_t *refcount,
+                             const int32_t *len, const int32_t *new_len,
+                             void *workspace, uint64_t ws_bytes, void *stream);
+
+/* Give back the pages of sequence b behind its first keep_len[b] rows (0: all
+ * of them; max_context: none): counts go down, entries become -1.
+ *   keep_len  device int32 [B], in [0, max_context] */
+kvc_status kvc_pages_free(kvc_cache *h, int32_t *block_table, int32_t *refcount,
+                          const int32_t *keep_len, void *stream);
+
+/* Copy whole blocks, every layer, K and V: block dst[i] becomes block src[i].
+ * Table and counts are not touched.
+ *   src, dst  device int32 [n], in [0, num_blocks); a pair out of range is
+ *             skipped and KVC_ERR_DEVICE_INDEX recorded.  A block that is a dst
+ *             must not be named a second time, as src or dst (its contents are
+ *             undefined otherwise)
+ *   n         >= 0 */
+kvc_status kvc_pages_copy(kvc_cache *h, const int32_t *src, const int32_t *dst, int32_t n, void *stream);
+
+/* Move all live pages (count > 0) into blocks [0, live): the live pages
+ * numbered live or higher go, in ascending order, to the free blocks below
+ * live in ascending order; rows, counts and table entries follow.
+ *   block_map  device int32 [num_blocks] or NULL; receives where each block's
+ *              contents went (its own number where they did not move), for a
+ *              caller that pins pages by number
+ *   n_live     device int32 [1], receives the number of live pages
+ *   workspace  device, ws_bytes >= kvc_pages_workspace_bytes */
+kvc_status kvc_pages_compact(kvc_cache *h, int32_t *block_table, int32_t *refcount,
+                             int32_t *block_map, int32_t *n_live, void *workspace,
+                             uint64_t ws_bytes, void *stream);
+
 /* ---- decode without any device allocation ------------------------------- */
 
 /* Size of the library's built-in scratch array used by kvc_decode_attn_static:

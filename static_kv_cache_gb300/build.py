@@ -37,7 +37,8 @@ def nvcc() -> str:
 
 def _units():
     units = []
-    for src in ("kvc_api.cu", "kvc_append.cu", "kvc_noalloc.cu", "kvc_mla_api.cu"):
+    for src in ("kvc_api.cu", "kvc_append.cu", "kvc_noalloc.cu", "kvc_mla_api.cu", "kvc_rows_api.cu",
+                "kvc_rows_simt.cu", "kvc_ingest.cu", "kvc_pages.cu"):
         units.append((os.path.join(CSRC, src), os.path.join(BUILD, src.replace(".cu", ".o")), []))
     inst = os.path.join(CSRC, "kvc_decode_inst.cu")
     for tag, code in ELEM_TYPES.items():

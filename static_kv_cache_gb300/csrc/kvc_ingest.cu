@@ -1,0 +1,206 @@
+// kvc_ingest.cu -- new rows into the cache other than one run per sequence:
+// packed prompts of different lengths, and the accepted path of a drafted tree.
+//
+// Both are copies of whole rows (row_vecs 16-byte vectors, consecutive lanes
+// on consecutive vectors on both sides) whose destination is looked up once per
+// row; K and V go in one launch, the path commit takes every layer in one.  Of
+// an int8 cache each row is quantised by one warp as kvc_append does it.
+#include <cuda_bf16.h>
+
+#include "kvc_rows.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int TOKENS = 8;  // tokens of a packed-append block
+
+// Cache row (in rows of a layer's slab or pool, KV head 0) of position pos of
+// sequence b and the distance between KV heads; false where the table has none.
+__device__ __forceinline__ bool cache_row(const IngestArgs &a, int b, int pos, int64_t &row, int64_t &head_step) {
+    if (!a.block_table) {
+        row = int64_t(b) * a.H_kv * a.max_ctx + pos;
+        head_step = a.max_ctx;
+        return true;
+    }
+    const int phys = __ldg(a.block_table + int64_t(b) * a.max_blocks + pos / 16);
+    row = int64_t(phys) * a.H_kv * 16 + pos % 16;
+    head_step = 16;
+    return phys >= 0 && phys < a.num_blocks;
+}
+
+// One row of D bf16 elements, quantised by a warp into codes and a scale.
+template <int D>
+__device__ __forceinline__ void store_q8(const uint8_t *src, uint8_t *codes, float *scale, int lane) {
+    constexpr int EPL = D / 32;
+    const __nv_bfloat16 *x16 = reinterpret_cast<const __nv_bfloat16 *>(src) + lane * EPL;
+    float x[EPL], sc;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) x[e] = __bfloat162float(x16[e]);
+    const uint32_t packed = dev::quantise_row_q8<EPL>(x, sc);
+    static_assert(EPL == 4, "four codes per lane");
+    reinterpret_cast<uint32_t *>(codes)[lane] = packed;
+    if (lane == 0) *scale = sc;
+}
+
+// The sequences' tokens in chunks of TOKENS, sequence after sequence: a block
+// finds its chunk by a prefix sum over the sequences' chunk counts, 256
+// sequences at a time.
+template <bool INT8>
+__global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constant__ IngestArgs a) {
+    __shared__ int warp_sum[8];
+    __shared__ int found_s[4];  // sequence, first token of the chunk in it, tokens, cache position of that token
+    __shared__ int64_t row_s[TOKENS], step_s[TOKENS];
+    dev::grid_dependency_wait();
+    dev::allow_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t chunk = blockIdx.x;; chunk += gridDim.x) {
+        int64_t base = 0;  // chunks of the sequences before this batch
+        bool found = false;
+        for (int b0 = 0; b0 < a.B && !found; b0 += 256) {
+            const int b = b0 + threadIdx.x;
+            int lo = 0, n = 0, c = 0;
+            if (b < a.B) {
+                lo = __ldg(a.cu_seqlens + b);
+                const int hi = __ldg(a.cu_seqlens + b + 1);
+                c = a.cache_index ? __ldg(a.cache_index + b) : 0;
+                const bool bad = lo < 0 || hi < lo || hi > a.total || c < 0 || c > a.max_ctx || hi - lo > a.max_ctx - c;
+                if (bad && chunk == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
+                n = bad ? 0 : hi - lo;
+            }
+            const int mine = (n + TOKENS - 1) / TOKENS;
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            __syncthreads();  // the last batch's (chunk's) shared values are read
+            if (lane == 31) warp_sum[warp] = incl;
+            __syncthreads();
+            int64_t first = base + incl - mine, all = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w < warp) first += warp_sum[w];
+                all += warp_sum[w];
+            }
+            if (chunk >= first && chunk < first + mine) {
+                const int t = int(chunk - first) * TOKENS;
+                found_s[0] = b;
+                found_s[1] = lo + t;
+                found_s[2] = n - t < TOKENS ? n - t : TOKENS;
+                found_s[3] = c + t;
+            }
+            base += all;
+            found = chunk < base;
+        }
+        if (!found) return;
+        __syncthreads();
+        const int t0 = found_s[1], nt = found_s[2];
+        if (threadIdx.x < nt) {
+            int64_t row, step;
+            if (!cache_row(a, found_s[0], found_s[3] + threadIdx.x, row, step)) {
+                dev::record_error(a.err, ERR_DEVICE_INDEX);
+                row = -1;
+            }
+            row_s[threadIdx.x] = row;
+            step_s[threadIdx.x] = step;
+        }
+        __syncthreads();
+        if constexpr (INT8) {
+            for (int x = warp; x < nt * a.H_kv * 2; x += 8) {
+                const int i = x / (2 * a.H_kv), j = (x >> 1) % a.H_kv;
+                const bool is_v = x & 1;
+                const int64_t row = row_s[i] + j * step_s[i];
+                store_q8<128>((is_v ? a.v_new : a.k_new) + ((int64_t(t0) + i) * a.H_kv + j) * 256, (is_v ? a.V : a.K) + row * 128,
+                              (is_v ? a.v_scale : a.k_scale) + row, lane);
+            }
+        } else {
+            const int per = a.H_kv * a.row_vecs;  // vectors of a token
+            for (int x = threadIdx.x; x < nt * per; x += blockDim.x) {
+                const int i = x / per, y = x - i * per, j = y / a.row_vecs, v = y - j * a.row_vecs;
+                if (row_s[i] < 0) continue;
+                const int64_t to = (row_s[i] + j * step_s[i]) * a.row_vecs + v, from = (int64_t(t0) + i) * per + y;
+                const uint4 kk = __ldg(reinterpret_cast<const uint4 *>(a.k_new) + from);
+                const uint4 vv = __ldg(reinterpret_cast<const uint4 *>(a.v_new) + from);
+                reinterpret_cast<uint4 *>(a.K)[to] = kk;
+                reinterpret_cast<uint4 *>(a.V)[to] = vv;
+            }
+        }
+    }
+}
+
+// A warp takes eight path positions of one (layer, K or V, sequence, KV head).
+constexpr int STEPS = 8;
+
+template <bool INT8>
+__global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ IngestArgs a) {
+    dev::grid_dependency_wait();
+    dev::allow_dependents();
+    const int lane = threadIdx.x & 31;
+    const int chunks = (a.P + STEPS - 1) / STEPS;
+    const int64_t segs = int64_t(a.B) * a.H_kv, units = 2 * segs * a.n_layers * chunks;
+    for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 8) {
+        const int64_t w = u / chunks;
+        const int chunk = int(u - w * chunks);
+        const bool is_v = w & 1;
+        const int64_t ls = w >> 1;                 // layer * segs + seg
+        const int layer = int(ls / segs), seg = int(ls - layer * segs), b = seg / a.H_kv, kv = seg - b * a.H_kv;
+        const int n = __ldg(a.n_accept + b), c = __ldg(a.cache_index + b);
+        bool bad = n < 0 || n > a.P || c < 0 || c > a.max_ctx || n > a.max_ctx - c;
+        if (!bad) {
+            for (int i = lane; i < n; i += 32) {
+                const int s = __ldg(a.path + int64_t(b) * a.P + i);
+                bad = bad || s < 0 || s >= a.T;
+            }
+            bad = __any_sync(0xffffffffu, bad);
+        }
+        if (bad) {
+            if (u == int64_t(b) * a.H_kv * 2 * chunks && lane == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
+            continue;
+        }
+        const uint8_t *src = (is_v ? a.v_new : a.k_new) + ls * a.T * a.row_vecs * 16;
+        uint8_t *dst = (is_v ? a.V : a.K) + layer * a.layer_bytes;
+        const int i0 = chunk * STEPS, steps = min(STEPS, n - i0);
+        if constexpr (INT8) {
+            float *sc = (is_v ? a.v_scale : a.k_scale) + layer * a.layer_scales;
+            for (int i = i0; i < i0 + steps; ++i) {
+                const int64_t row = int64_t(seg) * a.max_ctx + c + i;
+                store_q8<128>(src + int64_t(__ldg(a.path + int64_t(b) * a.P + i)) * 256, dst + row * 128, sc + row, lane);
+            }
+        } else {
+            for (int x = lane; x < steps * a.row_vecs; x += 32) {
+                const int i = i0 + x / a.row_vecs, v = x % a.row_vecs;
+                int64_t row, step;
+                if (!cache_row(a, b, c + i, row, step)) {
+                    dev::record_error(a.err, ERR_DEVICE_INDEX);
+                    continue;
+                }
+                const int64_t from = int64_t(__ldg(a.path + int64_t(b) * a.P + i)) * a.row_vecs + v;
+                reinterpret_cast<uint4 *>(dst)[(row + kv * step) * a.row_vecs + v] = __ldg(reinterpret_cast<const uint4 *>(src) + from);
+            }
+        }
+    }
+}
+
+int grid_of(int64_t want, int num_sms) {
+    const int64_t cap = int64_t(num_sms) * 8;
+    return int(want < cap ? want : cap);
+}
+
+}  // namespace
+
+cudaError_t launch_append_packed(const IngestArgs &a, bool int8, int num_sms, cudaStream_t s) {
+    // (every sequence may end inside a chunk)
+    const dim3 grid(grid_of(int64_t(a.total) / TOKENS + (a.B < a.total ? a.B : a.total), num_sms));
+    return int8 ? launch_pdl(append_packed_kernel<true>, grid, dim3(256), 0, s, a)
+                : launch_pdl(append_packed_kernel<false>, grid, dim3(256), 0, s, a);
+}
+
+cudaError_t launch_tree_commit(const IngestArgs &a, bool int8, int num_sms, cudaStream_t s) {
+    const int64_t units = 2ll * a.B * a.H_kv * a.n_layers * ((a.P + STEPS - 1) / STEPS);
+    const dim3 grid(grid_of((units + 7) / 8, num_sms));
+    return int8 ? launch_pdl(tree_commit_kernel<true>, grid, dim3(256), 0, s, a)
+                : launch_pdl(tree_commit_kernel<false>, grid, dim3(256), 0, s, a);
+}
+
+}  // namespace kvc

@@ -9,6 +9,7 @@
 namespace kvc {
 
 // Device error codes written to the workspace error word (match kvc_status).
+constexpr int32_t ERR_CAPACITY = 2;
 constexpr int32_t ERR_TIMEOUT = 5;
 constexpr int32_t ERR_DEVICE_INDEX = 6;
 

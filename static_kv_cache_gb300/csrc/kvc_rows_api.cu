@@ -1,0 +1,152 @@
+// kvc_rows_api.cu -- host side of the calls that take several new tokens per
+// sequence: argument checks and launch planning of kvc_prompt_attn,
+// kvc_append_packed, kvc_tree_attn and kvc_tree_commit.
+#include <cmath>
+
+#include "kvc_handle.cuh"
+#include "kvc_rows.cuh"
+
+namespace {
+
+bool device_current(const kvc_cache *h) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+// What both attentions fill in alike.
+kvc::RowsArgs rows_args(const kvc_cache *h, int32_t layer) {
+    const kvc_config &c = h->cfg;
+    const uint64_t slab = kvc::layer_slab_bytes(h);
+    kvc::RowsArgs a{};
+    a.K = h->k_base + slab * layer;
+    a.V = h->v_base + slab * layer;
+    a.block_table = h->block_table;
+    a.max_blocks = c.max_context / 16;
+    a.num_blocks = h->num_blocks;
+    a.err = reinterpret_cast<int32_t *>(h->ws);
+    a.B = c.batch;
+    a.H_kv = c.n_kv_heads;
+    a.group = h->group;
+    a.max_ctx = c.max_context;
+    a.scale_log2 = float(1.4426950408889634 / std::sqrt(double(c.d_head)));
+    return a;
+}
+
+kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &a, int max_tokens, void *stream) {
+    const cudaError_t e = kvc::launch_rows_simt(a, h->cfg.dtype, h->cfg.d_head, max_tokens, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+kvc::IngestArgs ingest_args(const kvc_cache *h, int32_t layer, const void *k, const void *v) {
+    const kvc_config &c = h->cfg;
+    const uint64_t slab = kvc::layer_slab_bytes(h);
+    kvc::IngestArgs a{};
+    a.K = h->k_base + slab * layer;
+    a.V = h->v_base + slab * layer;
+    a.layer_bytes = int64_t(slab);
+    if (h->k_scale) {
+        const uint64_t ss = kvc::layer_scale_bytes(h);
+        a.k_scale = reinterpret_cast<float *>(h->k_scale + ss * layer);
+        a.v_scale = reinterpret_cast<float *>(h->v_scale + ss * layer);
+        a.layer_scales = int64_t(ss / 4);
+    }
+    a.k_new = static_cast<const uint8_t *>(k);
+    a.v_new = static_cast<const uint8_t *>(v);
+    a.block_table = h->block_table;
+    a.max_blocks = c.max_context / 16;
+    a.num_blocks = h->num_blocks;
+    a.err = reinterpret_cast<int32_t *>(h->ws);
+    a.B = c.batch;
+    a.H_kv = c.n_kv_heads;
+    a.max_ctx = c.max_context;
+    a.row_vecs = c.d_head * (c.dtype == KVC_INT8 ? 2 : h->elem_bytes) / 16;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg) {
+    if (kvc_workspace_bytes(cfg) == 0) return 0;
+    return 256;
+}
+
+kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const void *k, const void *v,
+                           const int32_t *cu_seqlens, const int32_t *cache_index, int32_t total,
+                           void *workspace, uint64_t ws_bytes, void *out, void *stream) {
+    if (!h || layer < 0 || layer >= h->cfg.n_layers || total < 0) return KVC_ERR_INVALID;
+    if (h->cfg.dtype == KVC_INT8) return KVC_ERR_UNSUPPORTED;
+    if (total == 0) return KVC_OK;
+    if (!q || !k || !v || !cu_seqlens || !out || !device_current(h)) return KVC_ERR_INVALID;
+    if (!kvc::aligned16(q) || !kvc::aligned16(k) || !kvc::aligned16(v) || !kvc::aligned16(out)) return KVC_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < kvc_rows_workspace_bytes(&h->cfg)) return KVC_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KVC_ERR_ALIGNMENT;
+    kvc::RowsArgs a = rows_args(h, layer);
+    a.q = q;
+    a.k_new = k;
+    a.v_new = v;
+    a.out = out;
+    a.cu_seqlens = cu_seqlens;
+    a.cache_index = cache_index;
+    a.total = total;
+    return launch_rows(h, a, total, stream);
+}
+
+kvc_status kvc_append_packed(kvc_cache *h, int32_t layer, const void *k, const void *v,
+                             const int32_t *cu_seqlens, const int32_t *cache_index, int32_t total,
+                             void *stream) {
+    if (!h || layer < 0 || layer >= h->cfg.n_layers || total < 0) return KVC_ERR_INVALID;
+    if (total == 0) return KVC_OK;
+    if (!k || !v || !cu_seqlens || !device_current(h)) return KVC_ERR_INVALID;
+    if (!kvc::aligned16(k) || !kvc::aligned16(v)) return KVC_ERR_ALIGNMENT;
+    kvc::IngestArgs a = ingest_args(h, layer, k, v);
+    a.cu_seqlens = cu_seqlens;
+    a.cache_index = cache_index;
+    a.total = total;
+    const cudaError_t e = kvc::launch_append_packed(a, h->cfg.dtype == KVC_INT8, h->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_tree_attn(kvc_cache *h, int32_t layer, const void *q, const void *k_new, const void *v_new,
+                         const int32_t *cache_index, const int32_t *n_nodes, const uint32_t *tree_mask, int32_t T,
+                         int32_t max_index_hint, void *workspace, uint64_t ws_bytes, void *out, void *stream) {
+    if (!h || layer < 0 || layer >= h->cfg.n_layers || T < 1 || T > h->cfg.max_context || max_index_hint < 0 ||
+        max_index_hint > h->cfg.max_context)
+        return KVC_ERR_INVALID;
+    if (h->cfg.dtype == KVC_INT8) return KVC_ERR_UNSUPPORTED;
+    if (!q || !k_new || !v_new || !cache_index || !out || !device_current(h)) return KVC_ERR_INVALID;
+    if (!kvc::aligned16(q) || !kvc::aligned16(k_new) || !kvc::aligned16(v_new) || !kvc::aligned16(out)) return KVC_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < kvc_rows_workspace_bytes(&h->cfg)) return KVC_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KVC_ERR_ALIGNMENT;
+    kvc::RowsArgs a = rows_args(h, layer);
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.out = out;
+    a.cache_index = cache_index;
+    a.n_nodes = n_nodes;
+    a.tree_mask = tree_mask;
+    a.T = T;
+    a.mask_words = (T + 31) / 32;
+    return launch_rows(h, a, T, stream);
+}
+
+kvc_status kvc_tree_commit(kvc_cache *h, int32_t layer, int32_t n_layers, const void *k_new, const void *v_new,
+                           const int32_t *cache_index, const int32_t *path, const int32_t *n_accept, int32_t T,
+                           int32_t P, void *stream) {
+    if (!h || layer < 0 || n_layers < 1 || n_layers > h->cfg.n_layers - layer || T < 1 || P < 1) return KVC_ERR_INVALID;
+    if (!k_new || !v_new || !cache_index || !path || !n_accept || !device_current(h)) return KVC_ERR_INVALID;
+    if (!kvc::aligned16(k_new) || !kvc::aligned16(v_new)) return KVC_ERR_ALIGNMENT;
+    kvc::IngestArgs a = ingest_args(h, layer, k_new, v_new);
+    a.cache_index = cache_index;
+    a.path = path;
+    a.n_accept = n_accept;
+    a.n_layers = n_layers;
+    a.T = T;
+    a.P = P;
+    const cudaError_t e = kvc::launch_tree_commit(a, h->cfg.dtype == KVC_INT8, h->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -88,6 +88,28 @@ _lib.kvc_prefill_attn.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _vp]
 _lib.kvc_prefill_attn.restype = _i32
 _lib.kvc_decode_attn_static.argtypes = [_cfgp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp]
 _lib.kvc_decode_attn_static.restype = _i32
+_lib.kvc_rows_workspace_bytes.argtypes = [_cfgp]
+_lib.kvc_rows_workspace_bytes.restype = _u64
+_lib.kvc_prompt_attn.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _u64, _vp, _vp]
+_lib.kvc_prompt_attn.restype = _i32
+_lib.kvc_append_packed.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp]
+_lib.kvc_append_packed.restype = _i32
+_lib.kvc_tree_attn.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _u64, _vp, _vp]
+_lib.kvc_tree_attn.restype = _i32
+_lib.kvc_tree_commit.argtypes = [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp]
+_lib.kvc_tree_commit.restype = _i32
+_lib.kvc_pages_workspace_bytes.argtypes = [_cfgp, _i32]
+_lib.kvc_pages_workspace_bytes.restype = _u64
+_lib.kvc_pages_fork.argtypes = [_vp, _vp, _vp, _vp, _vp]
+_lib.kvc_pages_fork.restype = _i32
+_lib.kvc_pages_reserve.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _u64, _vp]
+_lib.kvc_pages_reserve.restype = _i32
+_lib.kvc_pages_free.argtypes = [_vp, _vp, _vp, _vp, _vp]
+_lib.kvc_pages_free.restype = _i32
+_lib.kvc_pages_copy.argtypes = [_vp, _vp, _vp, _i32, _vp]
+_lib.kvc_pages_copy.restype = _i32
+_lib.kvc_pages_compact.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _u64, _vp]
+_lib.kvc_pages_compact.restype = _i32
 _lib.kvc_get_error.argtypes = [_vp, _vp]
 _lib.kvc_get_error.restype = _i32
 _lib.kvc_static_get_error.argtypes = [_vp]
@@ -200,6 +222,60 @@ def kvc_decode_step(h, layer: int, q, k_new, v_new, valid_len, max_valid_hint: i
 def kvc_prefill_attn(h, layer: int, q, cache_index, T_new: int, out, stream=None) -> int:
     return _lib.kvc_prefill_attn(h, int(layer), _ptr(q), _ptr(cache_index), int(T_new), _ptr(out),
                                  _stream(stream))
+
+
+def kvc_rows_workspace_bytes(cfg: kvc_config) -> int:
+    return _lib.kvc_rows_workspace_bytes(ctypes.byref(cfg))
+
+
+def kvc_prompt_attn(h, layer: int, q, k, v, cu_seqlens, cache_index, total: int, workspace, ws_bytes: int, out,
+                    stream=None) -> int:
+    return _lib.kvc_prompt_attn(h, int(layer), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(cache_index),
+                                int(total), _ptr(workspace), int(ws_bytes), _ptr(out), _stream(stream))
+
+
+def kvc_append_packed(h, layer: int, k, v, cu_seqlens, cache_index, total: int, stream=None) -> int:
+    return _lib.kvc_append_packed(h, int(layer), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(cache_index), int(total),
+                                  _stream(stream))
+
+
+def kvc_tree_attn(h, layer: int, q, k_new, v_new, cache_index, n_nodes, tree_mask, T: int, max_index_hint: int,
+                  workspace, ws_bytes: int, out, stream=None) -> int:
+    return _lib.kvc_tree_attn(h, int(layer), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cache_index), _ptr(n_nodes),
+                              _ptr(tree_mask), int(T), int(max_index_hint), _ptr(workspace), int(ws_bytes),
+                              _ptr(out), _stream(stream))
+
+
+def kvc_tree_commit(h, layer: int, n_layers: int, k_new, v_new, cache_index, path, n_accept, T: int, P: int,
+                    stream=None) -> int:
+    return _lib.kvc_tree_commit(h, int(layer), int(n_layers), _ptr(k_new), _ptr(v_new), _ptr(cache_index),
+                                _ptr(path), _ptr(n_accept), int(T), int(P), _stream(stream))
+
+
+def kvc_pages_workspace_bytes(cfg: kvc_config, num_blocks: int) -> int:
+    return _lib.kvc_pages_workspace_bytes(ctypes.byref(cfg), int(num_blocks))
+
+
+def kvc_pages_fork(h, block_table, refcount, parent, stream=None) -> int:
+    return _lib.kvc_pages_fork(h, _ptr(block_table), _ptr(refcount), _ptr(parent), _stream(stream))
+
+
+def kvc_pages_reserve(h, block_table, refcount, length, new_len, workspace, ws_bytes: int, stream=None) -> int:
+    return _lib.kvc_pages_reserve(h, _ptr(block_table), _ptr(refcount), _ptr(length), _ptr(new_len),
+                                  _ptr(workspace), int(ws_bytes), _stream(stream))
+
+
+def kvc_pages_free(h, block_table, refcount, keep_len, stream=None) -> int:
+    return _lib.kvc_pages_free(h, _ptr(block_table), _ptr(refcount), _ptr(keep_len), _stream(stream))
+
+
+def kvc_pages_copy(h, src, dst, n: int, stream=None) -> int:
+    return _lib.kvc_pages_copy(h, _ptr(src), _ptr(dst), int(n), _stream(stream))
+
+
+def kvc_pages_compact(h, block_table, refcount, block_map, n_live, workspace, ws_bytes: int, stream=None) -> int:
+    return _lib.kvc_pages_compact(h, _ptr(block_table), _ptr(refcount), _ptr(block_map), _ptr(n_live),
+                                  _ptr(workspace), int(ws_bytes), _stream(stream))
 
 
 def kvc_decode_attn_static(cfg: kvc_config, layer: int, k_base, v_base, q, valid_len,

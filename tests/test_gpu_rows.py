@@ -1,0 +1,331 @@
+"""Prompt and tree attention on the GPU against their 64-bit definition.
+
+Cached rows past cache_index, new rows past a sequence's own, and packed rows
+outside every sequence hold NaN, outputs that must stay unwritten a canary
+value.  Tolerances are derived in oracle.rows.tolerance.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import rows
+from static_kv_cache_gb300 import synth
+from tests import _rows
+
+pytestmark = pytest.mark.gpu
+
+UNTOUCHED = 7.0
+
+
+def prompt(c, lens, cached, layer=0, gap=(0, 0), stream=None):
+    """Run kvc_prompt_attn; returns (packed q, k, v, cu, out buffer, out)."""
+    total = gap[0] + sum(lens) + gap[1]
+    cu = gap[0] + np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = c.draw(total, c.H, c.D, tag="q"), c.draw(total, c.G, c.D, tag="k"), c.draw(total, c.G, c.D, tag="v")
+    for x in (q, k, v):
+        x[:gap[0]] = float("nan")
+        x[total - gap[1]:] = float("nan")
+    kb, k = _rows.guarded(k)
+    vb, v = _rows.guarded(v)
+    ob, out = _rows.guarded(torch.full_like(q, UNTOUCHED))
+    st = c.kvc.kvc_prompt_attn(c.h, layer, q, k, v, _rows.ints(cu), None if cached is None else _rows.ints(cached), total,
+                               c.scratch.data, c.scratch.nbytes, out, stream)
+    return st, q, k, v, cu, (kb, vb, ob), out
+
+
+def check_prompt(c, lens, cached, layer=0, gap=(0, 0), skip=()):
+    st, q, k, v, cu, bufs, out = prompt(c, lens, cached, layer, gap)
+    assert st == 0
+    assert c.error() == (c.kvc.KVC_ERR_DEVICE_INDEX if skip else 0)
+    written = torch.zeros(len(q), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        if b in skip or n == 0:
+            continue
+        a, m = int(cu[b]), cached[b] if cached is not None else 0
+        written[a:a + n] = True
+        keys, vals = c.at(c.K, layer, b, range(m)), c.at(c.V, layer, b, range(m))
+        ref = rows.attend(q[a:a + n].transpose(0, 1), keys, vals, k[a:a + n].transpose(0, 1), v[a:a + n].transpose(0, 1),
+                          torch.ones(n, n, dtype=torch.bool).tril())
+        _rows.close(out[a:a + n].transpose(0, 1), *ref, c.dtype, c.D, m + n, f"sequence {b}")
+    assert (out.cpu()[~written] == UNTOUCHED).all()
+    assert c.intact() and all(x.canaries_intact() for x in bufs)
+
+
+def drafts(c, nodes, seen, T, gen_tag="t"):
+    q, k, v = c.draw(c.B, c.H, T, c.D, tag=gen_tag), c.draw(c.B, c.G, T, c.D, tag=gen_tag + "k"), c.draw(c.B, c.G, T, c.D, tag=gen_tag + "v")
+    for b, n in enumerate(nodes):
+        for x in (q, k, v):
+            x[b, :, n:] = float("nan")
+    return q, k, v
+
+
+def check_tree(c, T, cached, nodes, seen, layer=0, chain=False, hint=None, skip=(), stated_nodes=None, stated_cached=None):
+    n_of = [T] * c.B if nodes is None else nodes
+    q, k, v = drafts(c, n_of, seen, T)
+    kb, k = _rows.guarded(k)
+    vb, v = _rows.guarded(v)
+    ob, out = _rows.guarded(torch.full_like(q, UNTOUCHED))
+    said = stated_nodes if stated_nodes is not None else nodes
+    st = c.kvc.kvc_tree_attn(c.h, layer, q, k, v, _rows.ints(stated_cached if stated_cached is not None else cached),
+                             None if said is None else _rows.ints(said), None if chain else _rows.words(seen), T,
+                             max(cached) if hint is None else hint, c.scratch.data, c.scratch.nbytes, out, None)
+    assert st == 0
+    assert c.error() == (c.kvc.KVC_ERR_DEVICE_INDEX if skip else 0)
+    for b, n in enumerate(n_of):
+        if b in skip:
+            assert (out[b] == UNTOUCHED).all()
+            continue
+        assert (out[b, :, n:] == UNTOUCHED).all()
+        if n == 0:
+            continue
+        m = cached[b]
+        ref = rows.attend(q[b, :, :n], c.at(c.K, layer, b, range(m)), c.at(c.V, layer, b, range(m)), k[b, :, :n], v[b, :, :n],
+                          seen[b, :n, :n])
+        _rows.close(out[b, :, :n], *ref, c.dtype, c.D, m + n, f"sequence {b}")
+    assert c.intact() and all(x.canaries_intact() for x in (kb, vb, ob))
+
+
+# dtype, H, G, D: every kernel, groups that divide 128 and groups that do not
+SHAPES = [("bf16", 8, 2, 128), ("fp16", 6, 2, 128), ("bf16", 7, 1, 64), ("fp16", 2, 2, 64), ("bf16", 16, 1, 128),
+          ("fp16", 32, 1, 128), ("bf16", 64, 1, 64), ("bf16", 5, 1, 128), ("fp32", 4, 2, 64), ("bf16", 8, 2, 32),
+          ("fp16", 4, 1, 256), ("fp32", 2, 2, 128)]
+
+
+@pytest.mark.parametrize("dtype,H,G,D", SHAPES)
+def test_prompts_of_different_lengths(dtype, H, G, D):
+    c = _rows.Cache(dtype, 2, 6, H, G, D, 320, seed=1)
+    lens = [1, 0, 130, 17, 65, 2]
+    cached = [0, 40, 200, 3, 0, 129]
+    c.fill(1, cached)
+    check_prompt(c, lens, cached, layer=1, gap=(3, 5))
+    check_prompt(c, lens, None)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+def test_prompt_lengths_around_the_tiles(n):
+    c = _rows.Cache("bf16", 1, 2, 4, 1, 128, 16, seed=n)
+    check_prompt(c, [n, 3], None)
+
+
+@pytest.mark.parametrize("m", [1, 15, 16, 17, 127, 128, 129, 255, 256, 257, 383])
+@pytest.mark.parametrize("paged", [False, True])
+def test_prefix_lengths_around_the_tiles(m, paged):
+    c = _rows.Cache("fp16", 1, 2, 4, 1, 128, 400, paged=paged, seed=m)
+    c.fill(0, [m, 400])
+    check_prompt(c, [5, 40], [m, 400])
+
+
+@pytest.mark.parametrize("dtype,H,G,D", [("bf16", 8, 2, 128), ("fp16", 6, 2, 64), ("bf16", 32, 1, 128), ("fp16", 64, 1, 64), ("bf16", 7, 1, 128)])
+def test_paged_prompts(dtype, H, G, D):
+    c = _rows.Cache(dtype, 2, 4, H, G, D, 320, paged=True, seed=2)
+    cached = [320, 0, 33, 144]
+    c.fill(1, cached)
+    check_prompt(c, [20, 70, 150, 1], cached, layer=1)
+
+
+def test_one_prompt_split_over_the_gpu():
+    """One KV head and many key tiles: several CTAs share the rows."""
+    c = _rows.Cache("bf16", 1, 1, 4, 1, 128, 2048, seed=4)
+    c.fill(0, [2048])
+    check_prompt(c, [70], [2048])
+
+
+def test_bad_ranges_are_skipped():
+    c = _rows.Cache("bf16", 1, 4, 4, 2, 64, 64, seed=5)
+    c.fill(0, [10, 64, 20, 0])
+    q = c.draw(60, 4, 64, tag="q")
+    k, v = c.draw(60, 2, 64, tag="k"), c.draw(60, 2, 64, tag="v")
+    ob, out = _rows.guarded(torch.full_like(q, UNTOUCHED))
+    # sequence 0: cached rows out of range; 1: reversed; 2: past the end; 3 fine
+    for cu, cached, fine in (([0, 10, 20, 30, 60], [65, 64, -1, 0], (1, 3)), ([30, 40, 20, 61, 61], [0] * 4, (0,)),
+                             ([-1, 5, 60, 60, 59], [0] * 4, (1, 2))):
+        out.fill_(UNTOUCHED)
+        st = c.kvc.kvc_prompt_attn(c.h, 0, q, k, v, _rows.ints(cu), _rows.ints(cached), 60, c.scratch.data, c.scratch.nbytes, out, None)
+        assert st == 0 and c.error() == c.kvc.KVC_ERR_DEVICE_INDEX and c.error() == 0
+        written = torch.zeros(60, dtype=torch.bool)
+        for b in fine:
+            written[cu[b]:cu[b + 1]] = True
+        assert (out.cpu()[~written] == UNTOUCHED).all() and torch.isfinite(out.float()).all()
+        assert (out.cpu()[written] != UNTOUCHED).any(-1).all()
+    assert c.intact() and ob.canaries_intact()
+
+
+@pytest.mark.parametrize("dtype,H,G,D", SHAPES)
+def test_trees(dtype, H, G, D):
+    T = 21
+    c = _rows.Cache(dtype, 2, 5, H, G, D, 304, seed=6)
+    cached, nodes = [300, 0, 129, 64, 1], [21, 20, 0, 1, 13]
+    c.fill(1, cached)
+    seen = torch.stack([_rows.tree(T, s) for s in range(5)])
+    check_tree(c, T, cached, nodes, seen, layer=1)
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 64, 65, 100, 128, 129, 200, 260])
+def test_tree_sizes(T):
+    c = _rows.Cache("fp16", 1, 2, 4, 2, 64, 272, paged=True, seed=T)
+    c.fill(0, [130, 16])
+    seen = torch.stack([_rows.tree(T, T), _rows.tree(T, T + 1)])
+    check_tree(c, T, [130, 16], [T, max(1, T - 3)], seen, hint=0)
+
+
+@pytest.mark.parametrize("dtype,H,G,D", [("bf16", 8, 2, 128), ("fp16", 12, 2, 128), ("bf16", 32, 1, 64)])
+def test_paged_trees(dtype, H, G, D):
+    T = 40
+    c = _rows.Cache(dtype, 1, 3, H, G, D, 640, paged=True, seed=8)
+    c.fill(0, [640, 15, 333])
+    check_tree(c, T, [640, 15, 333], None, torch.stack([_rows.tree(T, s) for s in range(3)]))
+
+
+def test_a_chain_needs_no_mask():
+    c = _rows.Cache("bf16", 1, 2, 4, 1, 128, 300, seed=9)
+    c.fill(0, [300, 7])
+    seen = torch.stack([_rows.tree(50, 0, chain=True)] * 2)
+    check_tree(c, 50, [300, 7], [50, 33], seen, chain=True)
+
+
+def test_one_token_is_the_decode_step():
+    """T = 1: the decode attention of the row, were it appended."""
+    c = _rows.Cache("bf16", 1, 3, 8, 2, 128, 200, seed=10)
+    c.fill(0, [150, 1, 64])
+    check_tree(c, 1, [150, 1, 64], None, torch.ones(3, 1, 1, dtype=torch.bool))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_that_see_nothing_are_zero(dtype):
+    """Any mask: rows without a bit, rows that do not see themselves, bits of
+    tokens a sequence does not have."""
+    T = 37
+    c = _rows.Cache(dtype, 1, 3, 4, 2, 64, 64, seed=11)
+    c.fill(0, [0, 20, 0])
+    rng = np.random.default_rng(12)
+    seen = torch.from_numpy(rng.random((3, T, T)) < 0.2)
+    seen[:, 5] = False
+    seen[0, 30:] = False
+    seen[:, 36, 36] = False
+    check_tree(c, T, [0, 20, 0], [37, 37, 30], seen)
+
+
+def test_bad_tree_arguments_are_skipped():
+    c = _rows.Cache("bf16", 1, 4, 4, 2, 64, 64, seed=13)
+    c.fill(0, [10, 64, 20, 5])
+    seen = torch.stack([_rows.tree(9, s) for s in range(4)])
+    check_tree(c, 9, [10, 64, 20, 5], [9, 9, 4, 9], seen, skip=(1, 3), stated_nodes=[9, -1, 4, 10])
+    check_tree(c, 9, [10, 64, 20, 5], None, seen, skip=(0, 2), stated_cached=[65, 64, -1, 5])
+
+
+def test_a_page_out_of_range_is_recorded():
+    c = _rows.Cache("bf16", 1, 2, 8, 2, 128, 64, paged=True, seed=14)
+    c.fill(0, [60, 60])
+    good = c.table.clone()
+    for wrong in (-1, c.blocks, 2 ** 31 - 1):
+        c.table.copy_(good)
+        c.table[0, 2] = wrong
+        q, k, v = drafts(c, [4, 4], None, 4)
+        out = torch.zeros_like(q)
+        seen = torch.stack([_rows.tree(4, 1)] * 2)
+        assert c.kvc.kvc_tree_attn(c.h, 0, q, k, v, _rows.ints([60, 60]), None, _rows.words(seen), 4, 0, c.scratch.data,
+                                   c.scratch.nbytes, out, None) == 0
+        assert c.error() == c.kvc.KVC_ERR_DEVICE_INDEX
+        ref = rows.attend(q[1], c.at(c.K, 0, 1, range(60)), c.at(c.V, 0, 1, range(60)), k[1], v[1], seen[1])
+        _rows.close(out[1], *ref, "bf16", 128, 64)
+        # entries behind the cached rows are not looked at
+        c.table.copy_(good)
+        c.table[0, 2:] = wrong
+        assert c.kvc.kvc_tree_attn(c.h, 0, q, k, v, _rows.ints([32, 60]), None, _rows.words(seen), 4, 0, c.scratch.data,
+                                   c.scratch.nbytes, out, None) == 0
+        assert c.error() == 0
+    c.table.copy_(good)
+
+
+def test_refusals():
+    c = _rows.Cache("bf16", 2, 2, 4, 2, 64, 64, seed=15)
+    k, p = c.kvc, 256
+    big = 1 << 40
+    call = lambda **kw: k.kvc_prompt_attn(c.h, *[{**dict(layer=0, q=p, k=p, v=p, cu=p, c=None, total=8, ws=p, n=big, out=p), **kw}[x]  # noqa: E731
+                                                 for x in ("layer", "q", "k", "v", "cu", "c", "total", "ws", "n", "out")])
+    assert call(layer=2) == call(layer=-1) == call(total=-1) == call(q=None) == call(k=None) == call(v=None) == k.KVC_ERR_INVALID
+    assert call(cu=None) == call(out=None) == k.KVC_ERR_INVALID
+    assert call(q=p + 8) == call(k=p + 2) == call(v=p + 4) == call(out=p + 8) == call(ws=p + 16) == k.KVC_ERR_ALIGNMENT
+    assert call(ws=None) == call(n=k.kvc_rows_workspace_bytes(c.cfg) - 1) == k.KVC_ERR_WORKSPACE
+    assert call(total=0) == 0
+    call = lambda **kw: k.kvc_tree_attn(c.h, *[{**dict(layer=0, q=p, k=p, v=p, c=p, n=None, m=None, T=4, hint=0, ws=p, nb=big, out=p), **kw}[x]  # noqa: E731
+                                               for x in ("layer", "q", "k", "v", "c", "n", "m", "T", "hint", "ws", "nb", "out")])
+    assert call(layer=2) == call(T=0) == call(T=65) == call(hint=-1) == call(hint=65) == call(c=None) == k.KVC_ERR_INVALID
+    assert call(q=p + 8) == call(out=p + 2) == k.KVC_ERR_ALIGNMENT
+    assert call(ws=None) == call(nb=0) == k.KVC_ERR_WORKSPACE
+    assert k.kvc_append_packed(c.h, 2, p, p, p, p, 1) == k.kvc_append_packed(c.h, 0, p, p, None, p, 1) == k.KVC_ERR_INVALID
+    assert k.kvc_append_packed(c.h, 0, p + 8, p, p, p, 1) == k.KVC_ERR_ALIGNMENT
+    assert k.kvc_append_packed(c.h, 0, p, p, p, p, 0) == 0
+    for bad in ((0, 3, 4, 4), (1, 2, 4, 4), (0, 0, 4, 4), (0, 1, 0, 4), (0, 1, 4, 0)):
+        assert k.kvc_tree_commit(c.h, bad[0], bad[1], p, p, p, p, p, bad[2], bad[3]) == k.KVC_ERR_INVALID
+    assert k.kvc_tree_commit(c.h, 0, 1, p, p + 8, p, p, p, 4, 4) == k.KVC_ERR_ALIGNMENT
+    q8 = _rows.Cache("int8", 1, 2, 4, 2, 128, 64)
+    assert k.kvc_prompt_attn(q8.h, 0, p, p, p, p, None, 8, p, big, p) == k.KVC_ERR_UNSUPPORTED
+    assert k.kvc_tree_attn(q8.h, 0, p, p, p, p, None, None, 4, 0, p, big, p) == k.KVC_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("what", ["prompt", "tree"])
+def test_captured_and_replayed_on_another_stream(what):
+    """Two handles' calls in one graph, on a side stream, with one workspace in
+    stream order; the replay reads the inputs of the replay."""
+    a, b = (_rows.Cache("bf16", 1, 2, 8, 2, 128, 512, seed=s, paged=s == 21) for s in (20, 21))
+    for c in (a, b):
+        c.fill(0, [512, 77])
+    T = 24
+    seen = torch.stack([_rows.tree(T, 1), _rows.tree(T, 2)])
+    w, lens, cached = _rows.words(seen), _rows.ints([0, T, 2 * T]), _rows.ints([512, 77])
+    data = {}
+    for c in (a, b):
+        if what == "tree":
+            q, k, v = drafts(c, [T, T], None, T)
+        else:
+            q, k, v = c.draw(2 * T, c.H, c.D, tag="q"), c.draw(2 * T, c.G, c.D, tag="k"), c.draw(2 * T, c.G, c.D, tag="v")
+        data[c] = (q, k, v, torch.zeros_like(q))
+
+    def call(c, stream):
+        q, k, v, out = data[c]
+        if what == "tree":
+            st = c.kvc.kvc_tree_attn(c.h, 0, q, k, v, cached, None, w, T, 0, a.scratch.data, a.scratch.nbytes, out, stream)
+        else:
+            st = c.kvc.kvc_prompt_attn(c.h, 0, q, k, v, lens, cached, 2 * T, a.scratch.data, a.scratch.nbytes, out, stream)
+        assert st == 0
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call(a, side)
+            call(b, side)
+    for c in (a, b):
+        data[c][0].mul_(0.5)
+        data[c][3].fill_(UNTOUCHED)
+    torch.cuda.synchronize()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for c in (a, b):
+        q, k, v, out = data[c]
+        for s in range(2):
+            n = [512, 77][s]
+            if what == "tree":
+                x = (q[s], k[s], v[s], out[s], seen[s])
+            else:
+                x = [t[s * T:(s + 1) * T].transpose(0, 1) for t in (q, k, v, out)] + [torch.ones(T, T, dtype=torch.bool).tril()]
+            ref = rows.attend(x[0], c.at(c.K, 0, s, range(n)), c.at(c.V, 0, s, range(n)), x[1], x[2], x[4])
+            _rows.close(x[3], *ref, "bf16", 128, n + T)
+        assert c.error() == 0 and c.intact()
+
+
+def test_the_same_call_gives_the_same_bits():
+    c = _rows.Cache("bf16", 1, 3, 8, 2, 128, 1500, seed=30)
+    c.fill(0, [1500, 700, 3])
+    seen = torch.stack([_rows.tree(30, s) for s in range(3)])
+    q, k, v = drafts(c, [30] * 3, None, 30)
+    outs = []
+    for _ in range(5):
+        out = torch.zeros_like(q)
+        assert c.kvc.kvc_tree_attn(c.h, 0, q, k, v, _rows.ints([1500, 700, 3]), None, _rows.words(seen), 30, 0, c.scratch.data,
+                                   c.scratch.nbytes, out, None) == 0
+        outs.append(out.view(torch.int16).clone())
+    assert all(torch.equal(outs[0], x) for x in outs[1:])
