@@ -57,6 +57,11 @@ def _units():
         for d in (64, 128):
             obj = os.path.join(BUILD, f"kvc_prefill_{tag}_{d}.o")
             units.append((pre, obj, [f"-DKVC_INST_TYPE={code}", f"-DKVC_INST_D={d}"]))
+    rows = os.path.join(CSRC, "kvc_rows_inst.cu")
+    for code, tag in ((0, "bf16"), (1, "f16")):
+        for d in (64, 128):
+            units.append((rows, os.path.join(BUILD, f"kvc_rows_{tag}_{d}.o"),
+                          [f"-DKVC_INST_TYPE={code}", f"-DKVC_INST_D={d}"]))
     mla = os.path.join(CSRC, "kvc_mla_inst.cu")
     for code, tag in ((0, "bf16"), (1, "f16")):
         units.append((mla, os.path.join(BUILD, f"kvc_mla_{tag}.o"), [f"-DKVC_INST_TYPE={code}"]))

@@ -90,6 +90,18 @@ const kvc::PrefillKernelInfo *find_prefill(const kvc_config *c) {
     return nullptr;
 }
 
+// Tensor-core kernel of prompts and trees: 16-bit caches with d_h 64 or 128.
+const kvc::RowsKernelInfo *find_rows(const kvc_config *c) {
+    if (c->dtype == KVC_BF16) {
+        if (c->d_head == 64) return kvc::rows_kernel_bf16_64();
+        if (c->d_head == 128) return kvc::rows_kernel_bf16_128();
+    } else if (c->dtype == KVC_FP16) {
+        if (c->d_head == 64) return kvc::rows_kernel_f16_64();
+        if (c->d_head == 128) return kvc::rows_kernel_f16_128();
+    }
+    return nullptr;
+}
+
 }  // namespace
 
 const kvc::DecodeKernelInfo *kvc::find_decode_kernel(int32_t dtype, int D, int G) {
@@ -254,6 +266,26 @@ bool kvc::encode_pool_pair_maps(int32_t dtype, int D, int H_kv, int64_t blocks_t
     return true;
 }
 
+bool kvc::encode_pool_head_maps(int32_t dtype, int D, int H_kv, int64_t blocks_total, const void *k_pool,
+                                const void *v_pool, CUtensorMap *k, CUtensorMap *v) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode || (dtype != KVC_BF16 && dtype != KVC_FP16) || D % 64 != 0) return false;
+    const CUtensorMapDataType dt = dtype == KVC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t row = cuuint64_t(D) * 2;  // bytes of one row
+    const cuuint64_t dims[5] = {64, 16, cuuint64_t(D / 64), cuuint64_t(H_kv), cuuint64_t(blocks_total)};
+    const cuuint64_t strides[4] = {row, 128, 16 * row, cuuint64_t(H_kv) * 16 * row};
+    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    const cuuint32_t box[5] = {64, 16, cuuint32_t(D / 64), 1, 1};
+    const void *bases[2] = {k_pool, v_pool};
+    CUtensorMap *outs[2] = {k, v};
+    for (int i = 0; i < 2; ++i)
+        if (encode(outs[i], dt, 5, const_cast<void *>(bases[i]), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
 extern "C" {
 
 int32_t kvc_abi_version(void) { return KVC_ABI_VERSION; }
@@ -341,6 +373,9 @@ kvc_status alloc_impl(const kvc_config *cfg, void *k_base, void *v_base, void *k
     if (info->set_max_smem(smem_bytes) != cudaSuccess) return KVC_ERR_CUDA;
     if (pinfo && pinfo->set_max_smem(pinfo->smem) != cudaSuccess) return KVC_ERR_CUDA;
 
+    const kvc::RowsKernelInfo *rinfo = block_table || pinfo ? find_rows(cfg) : nullptr;
+    if (rinfo && rinfo->set_max_smem() != cudaSuccess) return KVC_ERR_CUDA;
+
     // Zero the workspace: error word and per-segment counters start at 0.
     if (cudaMemsetAsync(workspace, 0, need, 0) != cudaSuccess) return KVC_ERR_CUDA;
     if (cudaStreamSynchronize(0) != cudaSuccess) return KVC_ERR_CUDA;
@@ -367,6 +402,7 @@ kvc_status alloc_impl(const kvc_config *cfg, void *k_base, void *v_base, void *k
     h->wl = kvc::workspace_layout(cfg->batch, cfg->n_kv_heads / h->kv_pair, h->group * h->kv_pair, cfg->d_head);
     h->decode = info;
     h->prefill = pinfo;
+    h->rows = rinfo;
     h->n_stages = n_stages;
     h->smem_bytes = smem_bytes;
     if (block_table) {
@@ -378,7 +414,9 @@ kvc_status alloc_impl(const kvc_config *cfg, void *k_base, void *v_base, void *k
                                              &h->tm_k8, &h->tm_v32, &h->tm_v8)
                 : kvc::encode_pool_maps(cfg->dtype, cfg->d_head, int64_t(cfg->n_layers) * num_blocks * cfg->n_kv_heads,
                                         k_base, v_base, &h->tm_k32, &h->tm_k8, &h->tm_v32, &h->tm_v8);
-        if (!maps_ok) {
+        if (!maps_ok || (rinfo && !kvc::encode_pool_head_maps(cfg->dtype, cfg->d_head, cfg->n_kv_heads,
+                                                             int64_t(cfg->n_layers) * num_blocks, k_base, v_base,
+                                                             &h->rows_k, &h->rows_v))) {
             delete h;
             return KVC_ERR_CUDA;
         }
@@ -405,6 +443,8 @@ kvc_status alloc_impl(const kvc_config *cfg, void *k_base, void *v_base, void *k
             delete h;
             return KVC_ERR_CUDA;
         }
+        h->rows_k = h->pf_k128;  // (the two kernels cover the same types and widths)
+        h->rows_v = h->pf_v128;
         if (info->ragged_maps &&
             (!kvc::encode_row_box_maps(cfg->dtype, cfg->d_head, cfg->max_context, n_segs, k_base, v_base, 64,
                                        &h->rb_k64, &h->rb_v64) ||

@@ -8,6 +8,7 @@
 
 #include "../../include/kvc.h"
 #include "kvc_internal.cuh"
+#include "kvc_rows.cuh"
 
 struct kvc_cache {
     kvc_config cfg;
@@ -36,6 +37,8 @@ struct kvc_cache {
     CUtensorMap pf_k32, pf_k8, pf_v32, pf_v8;  // the chunked prefill's (64-column blocks)
     CUtensorMap pf_k128, pf_v128;             // and its whole-tile boxes (128 rows)
     CUtensorMap rb_k64, rb_v64, rb_k32, rb_v32;  // kernels with info->ragged_maps: 64- and 32-row boxes
+    const kvc::RowsKernelInfo *rows;          // prompts and trees on the tensor cores; nullptr: on the CUDA cores
+    CUtensorMap rows_k, rows_v;               // its maps of the cache: 128-row boxes, or whole blocks of one KV head
 };
 
 namespace kvc {

@@ -64,6 +64,44 @@ __device__ __forceinline__ int64_t rows_offset(const RowsArgs &a, const RowsSeq 
     return (a.cu_seqlens ? (s.row0 + t) * heads + h : (int64_t(b) * heads + h) * a.T + t) * D;
 }
 
+// What a CTA leaves for the combine when it starts an item that others go on
+// with (pieces 0: it does not).
+struct RowsCut {
+    int pieces;
+    int b, kv, t0, ntok;
+};
+
+// The tensor-core kernel's arguments (kvc_rows_tc.cuh).
+constexpr int ROWS_MAX_CTAS = 160;  // sizes the workspace
+struct RowsTcArgs : RowsArgs {
+    RowsCut *cuts;               // [grid]
+    float *part_ml;              // [2 grid][256][2]: (max, sum) of a piece's query rows
+    float *part_acc;             // [2 grid][256][D]: their unnormalised accumulators
+    int32_t min_share;           // key tiles of a CTA's share, at least
+    int32_t split_min;           // items of at most so many key tiles are not cut
+    int32_t seg_base;            // tensor-map segment (block) of the layer's first: layer * B * H_kv (layer * num_blocks)
+    int32_t pool_end;            // paged: one past the map's last block
+    unsigned long long timeout_ns;
+    CUtensorMap tm_k, tm_v;          // the cache: (D, T_max, segments) or the pool: (64, 16, D / 64, H_kv, blocks)
+    CUtensorMap tm_k_new, tm_v_new;  // new rows: (D, H_kv, total) packed, (D, T, B H_kv) dense
+};
+
+struct RowsKernelInfo {
+    cudaError_t (*set_max_smem)();
+    cudaError_t (*launch)(const RowsTcArgs &a, int grid, int combine_rows, cudaStream_t s);
+};
+// 16-bit caches with D = 64 or 128
+const RowsKernelInfo *rows_kernel_bf16_64();
+const RowsKernelInfo *rows_kernel_bf16_128();
+const RowsKernelInfo *rows_kernel_f16_64();
+const RowsKernelInfo *rows_kernel_f16_128();
+
+inline uint64_t rows_workspace(int D, uint64_t *ml, uint64_t *acc) {
+    *ml = align256(ROWS_MAX_CTAS * sizeof(RowsCut));
+    *acc = *ml + 2ull * ROWS_MAX_CTAS * 256 * 2 * 4;
+    return *acc + 2ull * ROWS_MAX_CTAS * 256 * D * 4;
+}
+
 cudaError_t launch_rows_simt(const RowsArgs &a, int dtype, int D, int max_tokens, cudaStream_t s);
 
 // Copies of new rows into the cache (kvc_ingest.cu).

@@ -32,8 +32,58 @@ kvc::RowsArgs rows_args(const kvc_cache *h, int32_t layer) {
     return a;
 }
 
-kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &a, int max_tokens, void *stream) {
-    const cudaError_t e = kvc::launch_rows_simt(a, h->cfg.dtype, h->cfg.d_head, max_tokens, static_cast<cudaStream_t>(stream));
+// A map of new rows with boxes of 128 rows x 64 columns: (D, H_kv, total) for
+// packed rows (the rows are the outermost dimension), (D, T, B * H_kv) for
+// dense ones.
+bool encode_new_rows(const kvc_cache *h, const kvc::RowsArgs &a, const void *base, CUtensorMap *out) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = kvc::tensor_map_encoder();
+    if (!encode) return false;
+    const bool packed = a.cu_seqlens != nullptr;
+    const cuuint64_t D = cuuint64_t(h->cfg.d_head);
+    const cuuint64_t d1 = packed ? a.H_kv : a.T, d2 = packed ? a.total : int64_t(a.B) * a.H_kv;
+    const cuuint64_t dims[3] = {D, d1, d2}, strides[2] = {2 * D, 2 * D * d1};
+    const cuuint32_t box[3] = {64, packed ? 1u : 128u, packed ? 128u : 1u}, elem[3] = {1, 1, 1};
+    return encode(out, h->cfg.dtype == KVC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// max_tokens: an upper bound on the new tokens of one sequence, max_cached on
+// its cached rows.
+kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int max_cached, int32_t layer, void *workspace,
+                       void *stream) {
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const kvc_config &c = h->cfg;
+    if (!h->rows) {
+        const cudaError_t e = kvc::launch_rows_simt(r, c.dtype, c.d_head, max_tokens, s);
+        return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+    }
+    kvc::RowsTcArgs a{};
+    static_cast<kvc::RowsArgs &>(a) = r;
+    if (!encode_new_rows(h, r, r.k_new, &a.tm_k_new) || !encode_new_rows(h, r, r.v_new, &a.tm_v_new)) return KVC_ERR_CUDA;
+    a.tm_k = h->rows_k;
+    a.tm_v = h->rows_v;
+    a.seg_base = layer * (h->block_table ? h->num_blocks : c.batch * c.n_kv_heads);
+    a.pool_end = c.n_layers * h->num_blocks;
+    a.timeout_ns = kvc::WAIT_TIMEOUT_NS;
+    uint64_t ml, acc;
+    kvc::rows_workspace(c.d_head, &ml, &acc);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.cuts = reinterpret_cast<kvc::RowsCut *>(ws);
+    a.part_ml = reinterpret_cast<float *>(ws + ml);
+    a.part_acc = reinterpret_cast<float *>(ws + acc);
+    // at most so many key tiles: of one item, and of all
+    const int ti = 2 * (128 / h->group);
+    const int64_t item = (max_cached + 127) / 128 + (int64_t(max_tokens) + 127) / 128;
+    a.min_share = 4;
+    a.split_min = item > 4 ? 4 : 0x7fffffff;  // (nothing is cut where no combine follows)
+    const int64_t blocks = r.cu_seqlens ? r.total / ti + (c.batch < r.total ? c.batch : r.total)
+                                        : int64_t(c.batch) * ((r.T + ti - 1) / ti);
+    const int64_t want = (blocks * c.n_kv_heads * item + a.min_share - 1) / a.min_share;
+    int64_t grid = h->num_sms < kvc::ROWS_MAX_CTAS ? h->num_sms : kvc::ROWS_MAX_CTAS;
+    if (want < grid) grid = want;
+    const int rows = (max_tokens < ti ? max_tokens : ti) * h->group;
+    const cudaError_t e = h->rows->launch(a, int(grid), item > 4 ? rows : 0, s);
     return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
@@ -69,7 +119,8 @@ extern "C" {
 
 uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg) {
     if (kvc_workspace_bytes(cfg) == 0) return 0;
-    return 256;
+    uint64_t ml, acc;
+    return kvc::rows_workspace(cfg->d_head, &ml, &acc);
 }
 
 kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const void *k, const void *v,
@@ -90,7 +141,7 @@ kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const voi
     a.cu_seqlens = cu_seqlens;
     a.cache_index = cache_index;
     a.total = total;
-    return launch_rows(h, a, total, stream);
+    return launch_rows(h, a, total, cache_index ? h->cfg.max_context : 0, layer, workspace, stream);
 }
 
 kvc_status kvc_append_packed(kvc_cache *h, int32_t layer, const void *k, const void *v,
@@ -129,7 +180,7 @@ kvc_status kvc_tree_attn(kvc_cache *h, int32_t layer, const void *q, const void 
     a.tree_mask = tree_mask;
     a.T = T;
     a.mask_words = (T + 31) / 32;
-    return launch_rows(h, a, T, stream);
+    return launch_rows(h, a, T, max_index_hint ? max_index_hint : h->cfg.max_context, layer, workspace, stream);
 }
 
 kvc_status kvc_tree_commit(kvc_cache *h, int32_t layer, int32_t n_layers, const void *k_new, const void *v_new,

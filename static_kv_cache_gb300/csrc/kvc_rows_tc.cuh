@@ -1,0 +1,899 @@
+// kvc_rows_tc.cuh -- attention of several new tokens per sequence on the
+// fifth-generation tensor cores (tcgen05, accumulators in tensor memory):
+// packed prompts and drafted trees over contiguous or paged caches, 16-bit
+// types, head widths 64 and 128.
+//
+// Work item: up to 2 TB new tokens (TB = 128 / g) of one (sequence, KV head)
+// as two tiles of 128 query rows that share every K and V tile -- tile x holds
+// tokens [t0 + x TB, t0 + (x + 1) TB), row r = i TB + tt of it is head i of the
+// group, token tt -- and the keys they can see in tiles of 128: the cached
+// rows, then the new rows.  Per key tile j and query tile x:
+//   S_x = Q_x . K_j^T    tcgen05.mma, M = 128, N = 128, K = d_h; both operands
+//                        K-major in shared memory
+//   softmax              one thread per query row (its TMEM lane): the row's
+//                        128 scores in registers, mask, running max and sum
+//                        in fp32 (log2 domain); the probabilities, rounded to
+//                        the cache type, overwrite S_x's columns
+//   O_x += P_x . V_j     tcgen05.mma with A = P_x from tensor memory, B = V_j
+//                        as stored (MN-major)
+// One thread issues all MMAs, in the order PV_A(j) S_A(j+1) PV_B(j) S_B(j+1):
+// while one query tile is in its softmax the tensor cores work on the other.
+// MMAs of one thread complete in order, so the barrier of S_x(j+1) also says
+// that PV_x(j) is done: the softmax may rescale O_x then, which it does only
+// when a tile's maximum exceeds the reference by more than 2^8.
+//
+// Split: all key tiles of all items form one line (item order: sequence, KV
+// head, token block) that is cut into equal shares, one per CTA, so that
+// ragged batches, long contexts with few rows and causal triangles all balance
+// with no planning on the host.  An item cut by a boundary leaves its
+// unnormalised accumulator and (max, sum) per piece in the workspace, and
+// rows_combine_kernel folds the pieces.
+//
+// Warps: 0-3 softmax and epilogue of tile A, 4-7 of tile B; 8 copies K and V
+// (one ring, in the order K_0 V_0 K_1 V_1 ...); 9 issues the MMAs and owns
+// tensor memory; 10 walks the items and hands them to the others; 10 and 11
+// copy the query rows.  Cached rows of a contiguous cache and new rows come as
+// boxes of 128 rows x 64 columns.  A page of 16 rows comes as one box of 16 rows
+// x d_h columns, laid out column block after column block: for d_h = 128 the
+// eight-row groups of a tile then lie 4096 bytes apart, so S takes the tile as
+// two MMAs of 64 keys (the upper and the lower halves of the eight pages) and
+// the score columns are in that order.
+//
+// A tile that is not full holds foreign rows behind its own: their scores are
+// masked, and their V rows are zeroed in shared memory before the PV (0 times
+// an infinity or NaN would not be 0).  In the same way the rows of a
+// partly visible tile are searched for infinities and NaN, which must reach
+// only the rows that see them: such elements are zeroed, and the epilogue of
+// the rows that see them adds them back.
+//
+// Every wait is bounded; a timeout records KVC_ERR_TIMEOUT, every role leaves
+// its loop, MMAs and copies in flight are waited for and tensor memory is freed
+// before the CTA exits.
+#pragma once
+
+#include <type_traits>
+
+#include "kvc_decode_mma.cuh"
+#include "kvc_prefill_tc.cuh"
+#include "kvc_rows.cuh"
+#include "kvc_tcgen05.cuh"
+
+namespace kvc {
+
+template <int D>
+struct RowsTcCfg {
+    static constexpr int BM = 128, BN = 128;
+    static constexpr int CB = D / 64;              // 128-byte column blocks of a row
+    static constexpr int ROW_BYTES = D * 2;
+    static constexpr int CHUNKS = ROW_BYTES / 16;
+    static constexpr int BLK = 128 * 128;          // one column block of a 128-row tile
+    static constexpr int TILE_BYTES = CB * BLK;    // a Q, K or V tile
+    static constexpr int NS = D == 64 ? 10 : 5;    // stages of the K / V ring
+    static constexpr int RING_OFF = 2 * TILE_BYTES;
+    static constexpr int BAR_OFF = RING_OFF + NS * TILE_BYTES;
+    // full[NS], empty[NS], s_full[2], p_full[2], o_full[2], o_free[2], q_full,
+    // q_empty, item_full[2], item_empty[2], mma_done
+    static constexpr int NBAR = 2 * NS + 15;
+    static constexpr int ITEM_OFF = BAR_OFF + 8 * NBAR + 8 + 32;  // after the TMEM address and the flags
+    static constexpr int SMEM = 1024 + ITEM_OFF + 2 * 64;
+    static constexpr int K_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10, Q_WARP = 11;
+    static constexpr int THREADS = 12 * 32;
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t S_COL = 0, O_COL = 256;  // S_A, S_B (128 columns each), O_A, O_B (D each)
+    static constexpr float RESCALE_LOG2 = 8.f;
+    static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+
+    // 16-byte chunk c of row r of a tile of 128 consecutive rows
+    __device__ __forceinline__ static uint32_t swz(uint32_t tile, int r, int c) {
+        return tile + uint32_t(c >> 3) * BLK + uint32_t(r) * 128 + (uint32_t((c & 7) ^ (r & 7)) << 4);
+    }
+    // the same for a tile of eight pages, each laid out column block after column block
+    __device__ __forceinline__ static uint32_t swz_paged(uint32_t tile, int r, int c) {
+        return tile + uint32_t(r >> 4) * (CB * 2048) + uint32_t(c >> 3) * 2048 + uint32_t(r & 15) * 128 +
+               (uint32_t((c & 7) ^ (r & 7)) << 4);
+    }
+};
+
+// A piece of work as the roles see it: tokens [t0, t0 + ntok) of (b, kv) against
+// key tiles [j0, j1).  b < 0: no more work.
+struct RowsItem {
+    int b, kv, t0, ntok;
+    int c, n, row0;   // the sequence: cached rows, new tokens, first packed row
+    int vis;          // new keys some row of the item sees: [0, vis)
+    int j0, j1;
+    int np;           // tiles of cached rows: tile j < np holds rows [128 j, ...), the others new rows
+    int slot;         // partial slot of a piece, -1: the whole item
+};
+static_assert(sizeof(RowsItem) <= 64, "item slot");
+
+// ---- the line of key tiles ------------------------------------------------------
+
+// Key tiles of the first q token blocks (of ti tokens) of one KV head of a
+// sequence: every block's cached tiles, and the new tiles its rows can see --
+// all of them under a mask, those up to its last token otherwise.
+__device__ __forceinline__ int64_t rows_prefix(const RowsArgs &a, const RowsSeq &s, int ti, int q) {
+    const int64_t np = (s.c + 127) / 128, kt = (s.n + 127) / 128;
+    if (a.tree_mask) return q * (np + kt);
+    const int nblk = (s.n + ti - 1) / ti;
+    if (ti > 128)  // 256 tokens: block k (from 1) sees 2 k tiles, the last one kt
+        return q * np + (q < nblk ? int64_t(q) * (q + 1) : int64_t(nblk) * (nblk - 1) + kt);
+    const int m = 128 / ti;
+    if (m * ti == 128) {  // m blocks a tile
+        const int64_t full = q / m, rest = q - full * m;
+        return q * np + m * full * (full + 1) / 2 + rest * (full + 1);
+    }
+    int64_t sum = q * np;
+    for (int k = 1; k <= q; ++k) sum += (min(s.n, k * ti) + 127) / 128;
+    return sum;
+}
+
+__device__ __forceinline__ int64_t rows_seq_tiles(const RowsArgs &a, const RowsSeq &s, int ti) {
+    return s.n == 0 ? 0 : rows_prefix(a, s, ti, (s.n + ti - 1) / ti);
+}
+
+__device__ __forceinline__ int rows_block_tiles(const RowsArgs &a, const RowsSeq &s, int ti, int qb) {
+    const int end = a.tree_mask ? s.n : min(s.n, (qb + 1) * ti);
+    return (s.c + 127) / 128 + (end + 127) / 128;
+}
+
+// Walks the items of a stretch of the line.  Taken by a whole warp.
+struct RowsWalk {
+    int b, kv, qb;
+    int64_t item0;      // start of the current item
+    RowsSeq s;
+    int64_t total;
+
+    __device__ __forceinline__ void total_of(const RowsArgs &a, int ti, int lane) {
+        int64_t sum = 0;
+        for (int i = lane; i < a.B; i += 32) sum += rows_seq_tiles(a, rows_seq(a, i), ti);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        total = sum * a.H_kv;
+    }
+
+    // Set the position to the item that holds tile x (x < total).
+    __device__ __forceinline__ void locate(const RowsArgs &a, int ti, int lane, int64_t at) {
+        int64_t base = 0;
+        int b0 = 0;
+        for (;; b0 += 32) {
+            const int i = b0 + lane;
+            const int64_t mine = i < a.B ? rows_seq_tiles(a, rows_seq(a, i), ti) * a.H_kv : 0;
+            int64_t incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > at);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                b = b0 + l;
+                const int64_t seq0 = base + __shfl_sync(0xffffffffu, incl - mine, l);
+                const int64_t per = __shfl_sync(0xffffffffu, mine, l) / a.H_kv;  // of one KV head
+                kv = int((at - seq0) / per);
+                item0 = seq0 + kv * per;
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        s = rows_seq(a, b);
+        if (128 % ti == 0 || ti > 128 || a.tree_mask) {  // the last block that starts at or before `at`
+            int lo = 0, hi = (s.n + ti - 1) / ti - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (item0 + rows_prefix(a, s, ti, mid) <= at) lo = mid; else hi = mid - 1;
+            }
+            qb = lo;
+            item0 += rows_prefix(a, s, ti, qb);
+        } else {
+            for (qb = 0;; ++qb) {
+                const int t = rows_block_tiles(a, s, ti, qb);
+                if (at < item0 + t) break;
+                item0 += t;
+            }
+        }
+    }
+
+    // The next item of the line follows the current one.
+    __device__ __forceinline__ void next(const RowsArgs &a, int ti) {
+        item0 += rows_block_tiles(a, s, ti, qb);
+        ++qb;
+        if (qb * int64_t(ti) < s.n) return;
+        qb = 0;
+        if (++kv < a.H_kv) return;
+        kv = 0;
+        do {
+            if (++b >= a.B) return;
+            s = rows_seq(a, b);
+        } while (s.n == 0);
+    }
+};
+
+// Start of CTA i's stretch: i shares in, moved back to the start of an item that
+// is too short to be worth cutting.
+__device__ __forceinline__ int64_t rows_boundary(const RowsTcArgs &a, RowsWalk &w, int ti, int lane, int64_t share, int i) {
+    const int64_t at = share * i;
+    if (at <= 0) return 0;
+    if (at >= w.total) return w.total;
+    w.locate(a, ti, lane, at);
+    return rows_block_tiles(a, w.s, ti, w.qb) <= a.split_min ? w.item0 : at;
+}
+
+__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void rows_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void rows_tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// One bit per score column of a tile: the keys [0, lim) of 128.
+__device__ __forceinline__ uint32_t lead_word(int lim, int k) {
+    const int m = lim - 32 * k;
+    return m >= 32 ? 0xffffffffu : m <= 0 ? 0u : (1u << m) - 1u;
+}
+// The same where the columns are the upper, then the lower halves of eight pages.
+__device__ __forceinline__ uint32_t lead_word_paged(int lim, int k) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int m = lim - (((4 * k + e) & 7) * 16 + (k >> 1) * 8);
+        w |= (m >= 8 ? 0xffu : m <= 0 ? 0u : (1u << m) - 1u) << (8 * e);
+    }
+    return w;
+}
+
+// Infinities and NaN among the eight 16-bit elements of a vector.
+template <typename T>
+__device__ __forceinline__ bool not_finite(const uint4 &v) {
+    constexpr uint32_t E = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad = bad || (w[i] & E) == E || ((w[i] >> 16) & E) == E;
+    return bad;
+}
+template <typename T>
+__device__ __forceinline__ uint4 finite_only(uint4 v) {
+    constexpr uint32_t E = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    uint32_t *w = &v.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & E) == E) w[i] &= 0xffff0000u;
+        if (((w[i] >> 16) & E) == E) w[i] &= 0x0000ffffu;
+    }
+    return v;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs a) {
+    using C = RowsTcCfg<D>;
+    using Ops = MmaOps<T>;
+    constexpr int BN = C::BN, CB = C::CB, NS = C::NS, BLK = C::BLK;
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t IDESC_S = tc::idesc_f16_f32acc(BF16, 128, BN, false, false);
+    constexpr uint32_t IDESC_S64 = tc::idesc_f16_f32acc(BF16, 128, 64, false, false);
+    constexpr uint32_t IDESC_O = tc::idesc_f16_f32acc(BF16, 128, D, false, true);
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = dev::smem_addr(smem);
+    const uint32_t ring = sb + C::RING_OFF;
+    const uint32_t full = sb + C::BAR_OFF, empty = full + 8 * NS, s_full = empty + 8 * NS, p_full = s_full + 16,
+                   o_full = p_full + 16, o_free = o_full + 16, q_full = o_free + 16, q_empty = q_full + 8,
+                   item_full = q_empty + 8, item_empty = item_full + 16, mma_done = item_empty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::NBAR);
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::BAR_OFF + 8 * C::NBAR + 8);  // abort, then odd[4]
+    volatile int *odd = flags + 1;  // item i met infinities or NaN: odd[i % 4]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.group, TB = 128 / G, TI = 2 * TB;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            dev::mbar_init(full + 8 * s, 1);
+            dev::mbar_init(empty + 8 * s, 1);  // the commit behind the stage's last MMA
+        }
+        for (int x = 0; x < 2; ++x) {
+            dev::mbar_init(s_full + 8 * x, 1);       // S_x is in tensor memory, PV_x before it done
+            dev::mbar_init(p_full + 8 * x, 4);       // the four softmax warps wrote P_x
+            dev::mbar_init(o_full + 8 * x, 1);       // the item's last PV_x is done
+            dev::mbar_init(o_free + 8 * x, 4);       // its accumulator is read
+            dev::mbar_init(item_full + 8 * x, 1);
+            dev::mbar_init(item_empty + 8 * x, 11);  // every role but the item warp has read the item (the second query warp too)
+        }
+        dev::mbar_init(q_full, 2);    // both query warps
+        dev::mbar_init(q_empty, 1);   // the item's last S has read Q
+        dev::mbar_init(mma_done, 1);
+        for (int i = 0; i < 5; ++i) flags[i] = 0;
+        dev::fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tc::tmem_alloc(dev::smem_addr(tmem_slot), C::TMEM_COLS);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    dev::grid_dependency_wait();
+    dev::allow_dependents();
+
+    auto give_up = [&]() {
+        if (lane == 0) {
+            if (!flags[0]) dev::record_error(a.err, ERR_TIMEOUT);
+            flags[0] = 1;
+        }
+    };
+    // the k-th item (k = 0, 1, ...) out of its slot; false on a timeout
+    auto take_item = [&](int k, RowsItem &it) {
+        const bool w = dev::mbar_wait_bounded(item_full + 8 * (k & 1), uint32_t(k >> 1) & 1, flags, a.timeout_ns);
+        if (!w) return false;
+        it = *reinterpret_cast<const RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1));
+        return true;
+    };
+    // one query tile's rows of an item into its Q buffer, by one warp
+    auto copy_q = [&](const RowsItem &it, int x) {
+        const int nt = min(TB, it.ntok - x * TB);
+        if (nt <= 0) return;
+        const int H = a.H_kv * G;
+        RowsSeq s;
+        s.row0 = it.row0;
+        const uint32_t qt = sb + x * C::TILE_BYTES;
+        const int total = G * nt * C::CHUNKS;
+        for (int i = lane; i < total; i += 32) {
+            const int c16 = i % C::CHUNKS, rr = i / C::CHUNKS, head = rr / nt, tt = rr - head * nt;
+            const T *src = reinterpret_cast<const T *>(a.q) + rows_offset(a, s, it.b, H, it.kv * G + head, it.t0 + x * TB + tt, D);
+            dev::cp_async_16(C::swz(qt, head * TB + tt, c16), reinterpret_cast<const uint4 *>(src) + c16);
+        }
+        cp_async_wait_all();
+        dev::fence_proxy_async_smem();
+    };
+
+    int issued = 0;  // stages filled by the copy warp
+    if (warp == C::ITEM_WARP) {
+        // ------------------------------------------------------------ items, and Q of tile A
+        if (blockIdx.x == 0)  // sequences whose arguments are out of range
+            for (int i = lane; i < a.B; i += 32)
+                if (rows_seq(a, i).bad) dev::record_error(a.err, ERR_DEVICE_INDEX);
+        RowsWalk w;
+        w.total_of(a, TI, lane);
+        const int grid = int(gridDim.x), me = int(blockIdx.x);
+        int64_t share = (w.total + grid - 1) / grid;
+        if (share < a.min_share) share = a.min_share;
+        const int64_t end = rows_boundary(a, w, TI, lane, share, me + 1);
+        const int64_t begin = rows_boundary(a, w, TI, lane, share, me);
+        RowsCut cut = {0, 0, 0, 0, 0};
+        bool ok = true;
+        if (begin < end) w.locate(a, TI, lane, begin);
+        int64_t at = begin;
+        for (int k = 0; ok; ++k) {
+            RowsItem it;
+            it.b = -1;
+            if (at < end) {
+                const int tiles = rows_block_tiles(a, w.s, TI, w.qb);
+                it.b = w.b;
+                it.kv = w.kv;
+                it.t0 = w.qb * TI;
+                it.ntok = min(TI, w.s.n - it.t0);
+                it.c = w.s.c;
+                it.n = w.s.n;
+                it.row0 = int(w.s.row0);
+                it.vis = a.tree_mask ? w.s.n : it.t0 + it.ntok;
+                it.np = (w.s.c + 127) / 128;
+                it.j0 = int(at - w.item0);
+                it.j1 = int(min(end - w.item0, int64_t(tiles)));
+                // pieces: the one that starts an item takes the CTA's second slot,
+                // one that goes on with it the first
+                it.slot = it.j0 == 0 && it.j1 == tiles ? -1 : 2 * me + (it.j0 == 0 ? 1 : 0);
+                if (it.j0 == 0 && it.j1 < tiles)
+                    cut = {int((w.item0 + tiles - 1) / share) - me + 1, it.b, it.kv, it.t0, it.ntok};
+                at = w.item0 + it.j1;
+                if (at < end) w.next(a, TI);
+            }
+            if (k >= 2) ok = __all_sync(FULL, dev::mbar_wait_bounded(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
+            if (!ok) break;
+            if (lane == 0) {
+                *reinterpret_cast<RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1)) = it;
+                dev::mbar_arrive(item_full + 8 * (k & 1));
+            }
+            if (it.b < 0) break;
+            if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
+            if (!ok) break;
+            copy_q(it, 0);
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(q_full);
+        }
+        if (lane == 0) a.cuts[me] = cut;
+        if (!ok) give_up();
+    } else if (warp == C::Q_WARP) {
+        // ------------------------------------------------------------ Q of tile B
+        bool ok = true;
+        RowsItem it;
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(FULL, take_item(k, it));
+            __syncwarp();
+            if (!ok) break;
+            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+            if (it.b < 0) break;
+            if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
+            if (!ok) break;
+            copy_q(it, 1);
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(q_full);
+        }
+        if (!ok) give_up();
+    } else if (warp == C::K_WARP) {
+        // ------------------------------------------------------------ K and V copies
+        bool ok = true;
+        RowsItem it;
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(FULL, take_item(k, it));
+            __syncwarp();
+            if (!ok) break;
+            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+            if (it.b < 0) break;
+            // a page's number is looked up a tile ahead
+            auto page_of = [&](int j) {
+                const int blk = 8 * j + lane;
+                if (!a.block_table || lane >= 8 || j >= min(it.np, it.j1) || blk * 16 >= it.c) return 0;
+                return __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk);
+            };
+            int next_page = page_of(it.j0);
+            for (int j = it.j0; ok && j < it.j1; ++j) {
+                const int page = next_page;
+                next_page = page_of(j + 1);
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int s = issued % NS;
+                    if (issued >= NS)
+                        ok = __all_sync(FULL, dev::mbar_wait_bounded(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
+                    if (!ok) break;
+                    const uint32_t dst = ring + uint32_t(s) * C::TILE_BYTES, bar = full + 8 * s;
+                    if (j >= it.np) {  // new rows
+                        const int jn = j - it.np;
+                        if (lane == 0) {
+                            dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                            const CUtensorMap *m = v ? &a.tm_v_new : &a.tm_k_new;
+#pragma unroll
+                            for (int cb = 0; cb < CB; ++cb)
+                                if (a.cu_seqlens)
+                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, it.kv, it.row0 + 128 * jn, bar);
+                                else
+                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * jn, it.b * a.H_kv + it.kv, bar);
+                        }
+                    } else if (!a.block_table) {
+                        if (lane == 0) {
+                            dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                            const CUtensorMap *m = v ? &a.tm_v : &a.tm_k;
+#pragma unroll
+                            for (int cb = 0; cb < CB; ++cb)
+                                dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * j, a.seg_base + it.b * a.H_kv + it.kv, bar);
+                        }
+                    } else {
+                        // the pages that hold cached rows, one lane each; a page out of
+                        // range is recorded and read as zeros (behind the pool's end)
+                        const int pages = min(8, (it.c - 128 * j + 15) / 16);
+                        if (lane == 0) dev::mbar_arrive_expect_tx(bar, uint32_t(pages) * CB * 2048);
+                        __syncwarp();
+                        if (lane < pages) {
+                            const bool in = page >= 0 && page < a.num_blocks;
+                            if (!in) dev::record_error(a.err, ERR_DEVICE_INDEX);
+                            dev::tma_load_5d(dst + lane * (CB * 2048), v ? &a.tm_v : &a.tm_k, 0, 0, 0, it.kv,
+                                             in ? a.seg_base + page : a.pool_end, bar);
+                        }
+                    }
+                    ++issued;
+                }
+            }
+        }
+        if (!ok) give_up();
+    } else if (warp == C::MMA_WARP) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0) {
+            bool ok = true;
+            RowsItem it;
+            uint32_t st = 0;           // stages consumed so far
+            uint32_t tiles[2] = {0, 0}, items[2] = {0, 0};  // of each query tile
+            auto stage_wait = [&](uint32_t i) { return dev::mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, flags, a.timeout_ns); };
+            auto issue_s = [&](int x, uint32_t i, bool paged) {
+                const uint32_t kt = ring + (i % NS) * C::TILE_BYTES, qt = sb + x * C::TILE_BYTES, s_t = tmem + C::S_COL + 128 * x;
+                if (CB == 2 && paged) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            tc::mma_f16_ss(s_t + 64 * h, tc::smem_desc_sw128(qt + (ks >> 2) * BLK + (ks & 3) * 32, 16, 1024),
+                                           tc::smem_desc_sw128(kt + (ks >> 2) * 2048 + (ks & 3) * 32 + h * 1024, 16, 4096), IDESC_S64, ks > 0);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc::mma_f16_ss(s_t, tc::smem_desc_sw128(qt + (ks >> 2) * BLK + (ks & 3) * 32, 16, 1024),
+                                       tc::smem_desc_sw128(kt + (ks >> 2) * BLK + (ks & 3) * 32, 16, 1024), IDESC_S, ks > 0);
+                }
+                tc::commit(s_full + 8 * x);
+            };
+            auto issue_pv = [&](int x, uint32_t i, bool paged, bool first) {
+                const uint32_t vt = ring + (i % NS) * C::TILE_BYTES, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint64_t desc = CB == 2 && paged ? tc::smem_desc_sw128(vt + (ks & 3) * 8192 + (ks >> 2) * 1024, 2048, 4096)
+                                                           : tc::smem_desc_sw128(vt + ks * 2048, BLK, 1024);
+                    tc::mma_f16_ts(o_t, p_t + 8 * ks, desc, IDESC_O, !first || ks > 0);
+                }
+            };
+            for (int k = 0; ok; ++k) {
+                ok = take_item(k, it);
+                if (!ok) break;
+                dev::mbar_arrive(item_empty + 8 * (k & 1));
+                if (it.b < 0) break;
+                const int nx = it.ntok > TB ? 2 : 1, n = it.j1 - it.j0;
+                auto is_paged = [&](int j) { return a.block_table && it.j0 + j < it.np; };
+                ok = dev::mbar_wait_bounded(q_full, uint32_t(k) & 1, flags, a.timeout_ns) && stage_wait(st);
+                if (!ok) break;
+                tc::fence_after();
+                for (int x = 0; x < nx; ++x) issue_s(x, st, is_paged(0));
+                tc::commit(empty + 8 * (st % NS));
+                if (n == 1) tc::commit(q_empty);
+                for (int j = 0; ok && j < n; ++j) {
+                    const uint32_t sv = st + 2 * j + 1, sk = sv + 1;
+                    for (int x = 0; x < nx; ++x) {
+                        ok = dev::mbar_wait_bounded(p_full + 8 * x, tiles[x] & 1, flags, a.timeout_ns);
+                        if (ok && x == 0) ok = stage_wait(sv);
+                        if (ok && j == 0 && items[x] > 0) ok = dev::mbar_wait_bounded(o_free + 8 * x, (items[x] - 1) & 1, flags, a.timeout_ns);
+                        if (!ok) break;
+                        ++tiles[x];
+                        tc::fence_after();
+                        issue_pv(x, sv, is_paged(j), j == 0);
+                        if (x == nx - 1) tc::commit(empty + 8 * (sv % NS));
+                        if (j + 1 < n) {
+                            if (x == 0) ok = stage_wait(sk);
+                            if (!ok) break;
+                            tc::fence_after();
+                            issue_s(x, sk, is_paged(j + 1));
+                            if (x == nx - 1) {
+                                tc::commit(empty + 8 * (sk % NS));
+                                if (j + 2 == n) tc::commit(q_empty);
+                            }
+                        } else {
+                            tc::commit(o_full + 8 * x);
+                            ++items[x];
+                        }
+                    }
+                }
+                st += 2 * n;
+            }
+            if (!ok) {
+                if (!flags[0]) dev::record_error(a.err, ERR_TIMEOUT);
+                flags[0] = 1;
+            }
+            tc::commit(mma_done);  // every MMA is done before tensor memory is freed
+            const volatile int never = 0;
+            dev::mbar_wait_bounded(mma_done, 0, &never, a.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax and epilogue
+        const int x = warp >> 2, qd = warp & 3;
+        const int r = 32 * qd + lane;           // query row = TMEM lane
+        const int head = r / TB, tt = r - head * TB;
+        const int H = a.H_kv * G;
+        const uint32_t lane_base = uint32_t(qd * 32) << 16;
+        const uint32_t s_t = tmem + lane_base + C::S_COL + 128 * x, o_t = tmem + lane_base + C::O_COL + D * x;
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+        bool ok = true;
+        uint32_t st = 0, gt = 0, gi = 0;  // ring position; tiles and items of this query tile so far
+        RowsItem it;
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(FULL, take_item(k, it));
+            __syncwarp();
+            if (!ok) break;
+            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+            if (it.b < 0) break;
+            const int n = it.j1 - it.j0;
+            if (x == 1 && it.ntok <= TB) {  // one query tile only
+                st += 2 * n;
+                continue;
+            }
+            // (the slot of item k - 3, which every role has left: it has taken item k - 2)
+            if (threadIdx.x == 0) odd[(k + 1) & 3] = 0;
+            const int t = it.t0 + x * TB + tt;              // token
+            const bool row_ok = head < G && x * TB + tt < it.ntok;
+            float m_run = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int j = 0; j < n; ++j, ++gt) {
+                ok = __all_sync(FULL, !flags[0] && dev::mbar_wait_bounded(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
+                if (!ok) break;
+                tc::fence_after();
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc::tmem_ld32(s_t + 32 * q, sr[q]);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc::reg_fence(sr[q]);
+                // ---- the keys of the tile that this row sees
+                const int jt = it.j0 + j;
+                const bool is_new = jt >= it.np;
+                const int key0 = 128 * (is_new ? jt - it.np : jt);       // first key, among the cached or the new rows
+                const int nv = min(128, (is_new ? it.vis : it.c) - key0);  // the tile's own rows
+                // does every row of the item see the whole tile?
+                const bool partial = nv < 128 || (is_new && (a.tree_mask || key0 + 127 > it.t0));
+                if (partial) {
+                    if (x == 0 && (nv < 128 || is_new)) {
+                        // V rows behind the tile's own are zeroed, infinities and NaN of
+                        // rows that not everybody sees set aside (PV_B follows PV_A, which
+                        // waits for these warps)
+                        const uint32_t sv = st + 2 * j + 1;
+                        ok = __all_sync(FULL, dev::mbar_wait_bounded(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns));
+                        if (!ok) break;
+                        const uint32_t vt = ring + (sv % NS) * C::TILE_BYTES;
+                        const bool paged = a.block_table && !is_new;
+#pragma unroll 1
+                        for (int i = r; i < 128 * C::CHUNKS; i += 128) {
+                            const int row = i / C::CHUNKS, c16 = i % C::CHUNKS;
+                            const uint32_t at = paged ? C::swz_paged(vt, row, c16) : C::swz(vt, row, c16);
+                            if (row >= nv) {
+                                dev::st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
+                            } else if (is_new) {
+                                uint4 v;
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+                                if (not_finite<T>(v)) {
+                                    odd[k & 3] = 1;
+                                    dev::st_shared_v4(at, finite_only<T>(v));
+                                }
+                            }
+                        }
+                        dev::fence_proxy_async_smem();
+                    }
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (!is_new)
+                            w[q] = CB == 2 && a.block_table ? lead_word_paged(nv, q) : lead_word(nv, q);
+                        else if (a.tree_mask)
+                            w[q] = row_ok && key0 / 32 + q < a.mask_words
+                                       ? __ldg(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + key0 / 32 + q) & lead_word(nv, q)
+                                       : 0u;
+                        else
+                            w[q] = lead_word(min(nv, t - key0 + 1), q);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(w[q] >> e & 1u)) sr[q][e] = __float_as_uint(-INFINITY);
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        m4[q] = fmax3(m4[q], __uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                // (a TMEM lane without a query row: whatever it holds stays in its lane)
+                const float m_tile = row_ok ? fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * a.scale_log2 : -INFINITY;
+                const float m_new = m_tile > m_run + C::RESCALE_LOG2 ? m_tile : m_run;
+                const float corr = m_new == m_run ? 1.f : ex2_approx(m_run - m_new);
+                m_run = m_new;
+                const float negm = m_run == -INFINITY ? 0.f : -m_run;
+                const float2 neg2 = make_float2(negm, negm);
+                if (j > 0 && __any_sync(FULL, corr != 1.f)) {
+                    // PV of the tile before is done (it precedes this S), the next waits for P
+                    const float2 c2 = make_float2(corr, corr);
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        rows_tmem_ld16(o_t + 16 * q, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), c2);
+                            o[e] = __float_as_uint(y.x);
+                            o[e + 1] = __float_as_uint(y.y);
+                        }
+                        rows_tmem_st16(o_t + 16 * q, o);
+                    }
+                }
+                float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1])), scale2, neg2);
+                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                        ps[(e >> 1) & 3] = __fadd2_rn(ps[(e >> 1) & 3], make_float2(p0, p1));
+                        pk[e / 2] = Ops::pack(p0, p1);
+                    }
+                    rows_tmem_st16(s_t + 16 * q, pk);  // over scores that are in registers
+                }
+                l2 = __ffma2_rn(l2, make_float2(corr, corr), __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3])));
+                tc::tmem_st_wait();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(p_full + 8 * x);
+            }
+            if (!ok) break;
+            st += 2 * n;
+            // ---- epilogue
+            ok = __all_sync(FULL, !flags[0] && dev::mbar_wait_bounded(o_full + 8 * x, gi & 1, flags, a.timeout_ns));
+            if (!ok) break;
+            ++gi;
+            tc::fence_after();
+            const bool any_odd = odd[k & 3] != 0;
+            const float l = l2.x + l2.y;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            RowsSeq sq;
+            sq.row0 = it.row0;
+            uint4 *orow = nullptr;
+            float *prow = nullptr;
+            if (row_ok) {
+                if (it.slot < 0) {
+                    orow = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + head, t, D));
+                } else {
+                    const int64_t row = int64_t(it.slot) * 256 + 128 * x + r;
+                    prow = a.part_acc + row * D;
+                    *reinterpret_cast<float2 *>(a.part_ml + 2 * row) = make_float2(m_run, l);
+                }
+            }
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tc::tmem_ld32(o_t + 32 * q, o);
+                tc::tmem_ld_wait();
+                tc::reg_fence(o);
+                if (q == D / 32 - 1) {  // the accumulator is read: the next item's PV may overwrite it
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) dev::mbar_arrive(o_free + 8 * x);
+                }
+                if (any_odd && row_ok) {
+                    // infinities and NaN among the V rows that this row sees (of
+                    // the tiles that were searched: those some row does not see whole)
+                    for (int jt = max(it.j0, it.np); jt < it.j1; ++jt) {
+                        const int key0 = 128 * (jt - it.np), nv = min(128, it.vis - key0);
+                        if (!(nv < 128 || a.tree_mask || key0 + 127 > it.t0)) continue;
+                        for (int s = 0; s < nv; ++s) {
+                            const int key = key0 + s;
+                            const bool see = a.tree_mask ? __ldg(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + (key >> 5)) >> (key & 31) & 1u
+                                                         : key <= t;
+                            if (!see) continue;
+                            const T *v = reinterpret_cast<const T *>(a.v_new) + rows_offset(a, sq, it.b, a.H_kv, it.kv, key, D) + 32 * q;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = float(v[e]);
+                                if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+                            }
+                        }
+                    }
+                }
+                if (orow) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = l > 0.f ? Ops::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv) : 0u;
+                        orow[4 * q + e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                } else if (prow) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) st_global_v8(prow + 32 * q + e, o + e);
+                }
+            }
+        }
+        if (!ok) give_up();
+    }
+
+    // ---- teardown
+    tc::fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+    if (warp == C::K_WARP && lane == 0 && flags[0]) {
+        // after an abort, wait (bounded) for the copies that may still land
+        const volatile int never = 0;
+        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+            dev::mbar_wait_bounded(full + 8 * (i % NS), uint32_t(i / NS) & 1, &never, a.timeout_ns);
+    }
+}
+
+// Folds the pieces of the items that CTA boundaries cut.  Block (i, y): rows
+// [8 y, 8 y + 8) of the item that CTA i started; a warp takes one row, with the
+// lanes on its columns:  out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsTcArgs a) {
+    constexpr int EPL = D / 32;
+    dev::grid_dependency_wait();
+    dev::allow_dependents();
+    const int i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const RowsCut cut = a.cuts[i];
+    if (cut.pieces == 0) return;
+    const int G = a.group, TB = 128 / G;
+    const int nt = blockIdx.y * 8 + warp;   // row of the item: (token, head)
+    if (nt >= cut.ntok * G) return;
+    const int tok = nt / G, head = nt - tok * G, x = tok / TB;
+    const int r = 128 * x + head * TB + (tok - x * TB);
+    auto row_of = [&](int p) { return int64_t(p == 0 ? 2 * i + 1 : 2 * (i + p)) * 256 + r; };
+    float M = -INFINITY;
+    for (int p = lane; p < cut.pieces; p += 32) M = fmaxf(M, __ldcg(a.part_ml + 2 * row_of(p)));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f, acc[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    if (M > -INFINITY) {
+        for (int p0 = 0; p0 < cut.pieces; p0 += 32) {
+            const int p = p0 + lane;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (p < cut.pieces) ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + 2 * row_of(p)));
+            const float e_lane = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+            float ll = ml.y * e_lane;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+            L += ll;
+            const int np = min(32, cut.pieces - p0);
+#pragma unroll 4
+            for (int q = 0; q < np; ++q) {
+                const float f = __shfl_sync(0xffffffffu, e_lane, q);
+                const float *src = a.part_acc + row_of(p0 + q) * D + lane * EPL;
+                if constexpr (EPL == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    acc[0] = fmaf(v.x, f, acc[0]), acc[1] = fmaf(v.y, f, acc[1]), acc[2] = fmaf(v.z, f, acc[2]), acc[3] = fmaf(v.w, f, acc[3]);
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    acc[0] = fmaf(v.x, f, acc[0]), acc[1] = fmaf(v.y, f, acc[1]);
+                }
+            }
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const RowsSeq s = rows_seq(a, cut.b);
+    T *o = reinterpret_cast<T *>(a.out) + rows_offset(a, s, cut.b, a.H_kv * G, cut.kv * G + head, cut.t0 + tok, D) + lane * EPL;
+    uint32_t u[EPL / 2];
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2) u[e / 2] = M > -INFINITY ? MmaOps<T>::pack(acc[e] * inv, acc[e + 1] * inv) : 0u;
+    if constexpr (EPL == 4)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(u[0], u[1]);
+    else
+        *reinterpret_cast<uint32_t *>(o) = u[0];
+}
+
+template <typename T, int D>
+cudaError_t set_rows_tc_max_smem() {
+    return cudaFuncSetAttribute(rows_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsTcCfg<D>::SMEM);
+}
+
+// combine_rows: query rows of the largest item; 0 where no item can be cut.
+template <typename T, int D>
+cudaError_t launch_rows_tc(const RowsTcArgs &a, int grid, int combine_rows, cudaStream_t s) {
+    const cudaError_t e = launch_pdl(rows_tc_kernel<T, D>, dim3(grid), dim3(RowsTcCfg<D>::THREADS), RowsTcCfg<D>::SMEM, s, a);
+    if (e != cudaSuccess || combine_rows == 0 || grid == 1) return e;
+    return launch_pdl(rows_combine_kernel<T, D>, dim3(grid, (combine_rows + 7) / 8), dim3(256), 0, s, a);
+}
+
+template <typename T, int D>
+const RowsKernelInfo *rows_tc_info() {
+    static const RowsKernelInfo info = {&set_rows_tc_max_smem<T, D>, &launch_rows_tc<T, D>};
+    return &info;
+}
+
+}  // namespace kvc
