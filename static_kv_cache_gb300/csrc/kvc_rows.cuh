@@ -84,6 +84,7 @@ struct RowsTcArgs : RowsArgs {
     unsigned long long timeout_ns;
     CUtensorMap tm_k, tm_v;          // the cache: (D, T_max, segments) or the pool: (64, 16, D / 64, H_kv, blocks)
     CUtensorMap tm_k_new, tm_v_new;  // new rows: (D, H_kv, total) packed, (D, T, B H_kv) dense
+    CUtensorMap tm_q;                // (D, H, total) packed, (D, H, T, B) dense: boxes of 64 columns, g heads, 128 / g tokens
 };
 
 struct RowsKernelInfo {

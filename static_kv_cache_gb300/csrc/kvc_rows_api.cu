@@ -48,6 +48,21 @@ bool encode_new_rows(const kvc_cache *h, const kvc::RowsArgs &a, const void *bas
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries' map, boxes of 128 / g tokens x g heads x 64 columns: a query
+// tile's rows, token after token, in either layout.
+bool encode_queries(const kvc_cache *h, const kvc::RowsArgs &a, CUtensorMap *out) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = kvc::tensor_map_encoder();
+    if (!encode) return false;
+    const bool packed = a.cu_seqlens != nullptr;
+    const cuuint64_t D = cuuint64_t(h->cfg.d_head), H = cuuint64_t(h->cfg.n_heads), T = cuuint64_t(a.T);
+    const cuuint64_t dims[4] = {D, H, packed ? cuuint64_t(a.total) : T, cuuint64_t(a.B)};
+    const cuuint64_t strides[3] = {packed ? 2 * D : 2 * D * T, packed ? 2 * D * H : 2 * D, 2 * D * H * T};
+    const cuuint32_t box[4] = {64, cuuint32_t(a.group), cuuint32_t(128 / a.group), 1}, elem[4] = {1, 1, 1, 1};
+    return encode(out, h->cfg.dtype == KVC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  packed ? 3 : 4, const_cast<void *>(a.q), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // max_tokens: an upper bound on the new tokens of one sequence, max_cached on
 // its cached rows.
 kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int max_cached, int32_t layer, void *workspace,
@@ -60,7 +75,9 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     }
     kvc::RowsTcArgs a{};
     static_cast<kvc::RowsArgs &>(a) = r;
-    if (!encode_new_rows(h, r, r.k_new, &a.tm_k_new) || !encode_new_rows(h, r, r.v_new, &a.tm_v_new)) return KVC_ERR_CUDA;
+    if (!encode_new_rows(h, r, r.k_new, &a.tm_k_new) || !encode_new_rows(h, r, r.v_new, &a.tm_v_new) ||
+        !encode_queries(h, r, &a.tm_q))
+        return KVC_ERR_CUDA;
     a.tm_k = h->rows_k;
     a.tm_v = h->rows_v;
     a.seg_base = layer * (h->block_table ? h->num_blocks : c.batch * c.n_kv_heads);

@@ -4,10 +4,14 @@
 // types, head widths 64 and 128.
 //
 // Work item: up to 2 TB new tokens (TB = 128 / g) of one (sequence, KV head)
-// as two tiles of 128 query rows that share every K and V tile -- tile x holds
-// tokens [t0 + x TB, t0 + (x + 1) TB), row r = i TB + tt of it is head i of the
-// group, token tt -- and the keys they can see in tiles of 128: the cached
-// rows, then the new rows.  Per key tile j and query tile x:
+// as two tiles of 128 query rows -- tile x holds tokens [t0 + x TB, t0 + (x + 1)
+// TB), row r = tt g + i of it is token tt, head i of the group, which is how
+// one box of a tensor map brings them in either layout -- and the keys they can
+// see in tiles of 128: the cached rows, then the new rows.  Both query tiles
+// share every K and V tile; an item with at most TB tokens has one query tile,
+// and two streams x share its key tiles instead, even ones and odd ones
+// ("folded": their accumulators are added at the end).  Per key tile j and
+// stream x:
 //   S_x = Q_x . K_j^T    tcgen05.mma, M = 128, N = 128, K = d_h; both operands
 //                        K-major in shared memory
 //   softmax              one thread per query row (its TMEM lane): the row's
@@ -16,11 +20,12 @@
 //                        the cache type, overwrite S_x's columns
 //   O_x += P_x . V_j     tcgen05.mma with A = P_x from tensor memory, B = V_j
 //                        as stored (MN-major)
-// One thread issues all MMAs, in the order PV_A(j) S_A(j+1) PV_B(j) S_B(j+1):
-// while one query tile is in its softmax the tensor cores work on the other.
-// MMAs of one thread complete in order, so the barrier of S_x(j+1) also says
-// that PV_x(j) is done: the softmax may rescale O_x then, which it does only
-// when a tile's maximum exceeds the reference by more than 2^8.
+// One warp issues all MMAs, in the order PV_A(j) S_A(j+1) PV_B(j) S_B(j+1)
+// (folded: PV_A(j) S_A(j+2) PV_B(j+1) S_B(j+3)): while one stream is in its
+// softmax the tensor cores work on the other.  MMAs of one thread complete in
+// order, so the barrier of a stream's next S also says that its PV is done: the
+// softmax may rescale O_x then, which it does only when a tile's maximum
+// exceeds the reference by more than 2^8.
 //
 // Split: all key tiles of all items form one line (item order: sequence, KV
 // head, token block) that is cut into equal shares, one per CTA, so that
@@ -29,10 +34,10 @@
 // unnormalised accumulator and (max, sum) per piece in the workspace, and
 // rows_combine_kernel folds the pieces.
 //
-// Warps: 0-3 softmax and epilogue of tile A, 4-7 of tile B; 8 copies K and V
-// (one ring, in the order K_0 V_0 K_1 V_1 ...); 9 issues the MMAs and owns
-// tensor memory; 10 walks the items and hands them to the others; 10 and 11
-// copy the query rows.  Cached rows of a contiguous cache and new rows come as
+// Warps: 0-3 softmax and epilogue of stream A, 4-7 of stream B; 8 copies K and V
+// (one ring, in the order in which the MMAs take them); 9 issues the MMAs and
+// owns tensor memory; 10 walks the items, hands them to the others and copies
+// their query rows.  Cached rows of a contiguous cache and new rows come as
 // boxes of 128 rows x 64 columns.  A page of 16 rows comes as one box of 16 rows
 // x d_h columns, laid out column block after column block: for d_h = 128 the
 // eight-row groups of a tile then lie 4096 bytes apart, so S takes the tile as
@@ -72,12 +77,13 @@ struct RowsTcCfg {
     static constexpr int RING_OFF = 2 * TILE_BYTES;
     static constexpr int BAR_OFF = RING_OFF + NS * TILE_BYTES;
     // full[NS], empty[NS], s_full[2], p_full[2], o_full[2], o_free[2], q_full,
-    // q_empty, item_full[2], item_empty[2], mma_done
-    static constexpr int NBAR = 2 * NS + 15;
-    static constexpr int ITEM_OFF = BAR_OFF + 8 * NBAR + 8 + 32;  // after the TMEM address and the flags
-    static constexpr int SMEM = 1024 + ITEM_OFF + 2 * 64;
-    static constexpr int K_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10, Q_WARP = 11;
-    static constexpr int THREADS = 12 * 32;
+    // q_empty, item_full[2], item_empty[2], fold, mma_done
+    static constexpr int NBAR = 2 * NS + 16;
+    static constexpr int ITEM_OFF = BAR_OFF + 8 * NBAR + 8 + 24;  // after the TMEM address and the flags
+    static constexpr int FOLD_OFF = ITEM_OFF + 2 * 64;            // folded items: stream A's (max, sum) of each row
+    static constexpr int SMEM = 1024 + FOLD_OFF + 128 * 8;
+    static constexpr int K_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10;
+    static constexpr int THREADS = 11 * 32;
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // S_A, S_B (128 columns each), O_A, O_B (D each)
     static constexpr float RESCALE_LOG2 = 8.f;
@@ -136,65 +142,18 @@ __device__ __forceinline__ int rows_block_tiles(const RowsArgs &a, const RowsSeq
     return (s.c + 127) / 128 + (end + 127) / 128;
 }
 
-// Walks the items of a stretch of the line.  Taken by a whole warp.
-struct RowsWalk {
+// 64-bit quotient; the values fit 32 bits but for enormous calls.
+__device__ __forceinline__ int64_t rows_div(int64_t x, int64_t y) {
+    return (uint64_t(x) | uint64_t(y)) >> 32 ? x / y : int64_t(uint32_t(x) / uint32_t(y));
+}
+
+// A place on the line: token block qb of (b, kv), whose key tiles start at
+// item0.
+struct RowsPlace {
     int b, kv, qb;
-    int64_t item0;      // start of the current item
+    int64_t item0;
     RowsSeq s;
-    int64_t total;
 
-    __device__ __forceinline__ void total_of(const RowsArgs &a, int ti, int lane) {
-        int64_t sum = 0;
-        for (int i = lane; i < a.B; i += 32) sum += rows_seq_tiles(a, rows_seq(a, i), ti);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        total = sum * a.H_kv;
-    }
-
-    // Set the position to the item that holds tile x (x < total).
-    __device__ __forceinline__ void locate(const RowsArgs &a, int ti, int lane, int64_t at) {
-        int64_t base = 0;
-        int b0 = 0;
-        for (;; b0 += 32) {
-            const int i = b0 + lane;
-            const int64_t mine = i < a.B ? rows_seq_tiles(a, rows_seq(a, i), ti) * a.H_kv : 0;
-            int64_t incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > at);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                b = b0 + l;
-                const int64_t seq0 = base + __shfl_sync(0xffffffffu, incl - mine, l);
-                const int64_t per = __shfl_sync(0xffffffffu, mine, l) / a.H_kv;  // of one KV head
-                kv = int((at - seq0) / per);
-                item0 = seq0 + kv * per;
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        s = rows_seq(a, b);
-        if (128 % ti == 0 || ti > 128 || a.tree_mask) {  // the last block that starts at or before `at`
-            int lo = 0, hi = (s.n + ti - 1) / ti - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (item0 + rows_prefix(a, s, ti, mid) <= at) lo = mid; else hi = mid - 1;
-            }
-            qb = lo;
-            item0 += rows_prefix(a, s, ti, qb);
-        } else {
-            for (qb = 0;; ++qb) {
-                const int t = rows_block_tiles(a, s, ti, qb);
-                if (at < item0 + t) break;
-                item0 += t;
-            }
-        }
-    }
-
-    // The next item of the line follows the current one.
     __device__ __forceinline__ void next(const RowsArgs &a, int ti) {
         item0 += rows_block_tiles(a, s, ti, qb);
         ++qb;
@@ -209,14 +168,85 @@ struct RowsWalk {
     }
 };
 
-// Start of CTA i's stretch: i shares in, moved back to the start of an item that
-// is too short to be worth cutting.
-__device__ __forceinline__ int64_t rows_boundary(const RowsTcArgs &a, RowsWalk &w, int ti, int lane, int64_t share, int i) {
-    const int64_t at = share * i;
-    if (at <= 0) return 0;
-    if (at >= w.total) return w.total;
-    w.locate(a, ti, lane, at);
-    return rows_block_tiles(a, w.s, ti, w.qb) <= a.split_min ? w.item0 : at;
+// This CTA's stretch [begin, end) of the line, `place` at its start, and the
+// share that cuts the line.  Boundary i is at i shares, moved back to the start
+// of an item that is too short to be worth cutting; even lanes of the warp work
+// out this CTA's boundary, odd lanes the next one's.
+__device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane, int64_t &share, int64_t &begin, int64_t &end,
+                                          RowsPlace &place) {
+    constexpr unsigned FULL = 0xffffffffu;
+    int64_t mine = 0, sum = 0;  // tiles of this lane's sequence (of the last batch of 32)
+    for (int i = lane; i < a.B; i += 32) sum += mine = rows_seq_tiles(a, rows_seq(a, i), ti) * a.H_kv;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    const int64_t total = sum;
+    share = rows_div(total + gridDim.x - 1, gridDim.x);
+    if (share < a.min_share) share = a.min_share;
+    const int64_t at = share * (blockIdx.x + (lane & 1));
+    const bool inside = at > 0 && at < total;
+    const int64_t at_a = __shfl_sync(FULL, at, 0), at_b = __shfl_sync(FULL, at, 1);
+    // the sequence that holds each
+    int64_t base = 0, seq0 = 0, per = 1;
+    int b = -1;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        if (a.B > 32) mine = b0 + lane < a.B ? rows_seq_tiles(a, rows_seq(a, b0 + lane), ti) * a.H_kv : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl += y;
+        }
+        incl += base;
+        const unsigned hit_a = __ballot_sync(FULL, incl > at_a), hit_b = __ballot_sync(FULL, incl > at_b);
+        const unsigned hit = lane & 1 ? hit_b : hit_a;
+        const int l = hit ? __ffs(hit) - 1 : 0;
+        const int64_t tiles = __shfl_sync(FULL, mine, l), last = __shfl_sync(FULL, incl, l);
+        if (hit && b < 0) {
+            b = b0 + l;
+            per = rows_div(tiles, a.H_kv);
+            seq0 = last - tiles;
+        }
+        base = __shfl_sync(FULL, incl, 31);
+        if (hit_a && hit_b) break;
+    }
+    RowsPlace p;
+    p.b = b;
+    p.kv = p.qb = 0;
+    p.item0 = 0;
+    int64_t bound = at <= 0 ? 0 : total;
+    if (b >= 0) {
+        p.s = rows_seq(a, b);
+        p.kv = int(rows_div(at - seq0, per));
+        p.item0 = seq0 + p.kv * per;
+        const int nblk = (p.s.n + ti - 1) / ti;
+        // the last block that starts at or before `at`
+        if (a.tree_mask) {
+            p.qb = int(rows_div(at - p.item0, rows_block_tiles(a, p.s, ti, 0)));
+            p.item0 += rows_prefix(a, p.s, ti, p.qb);
+        } else if (128 % ti == 0 || ti > 128) {
+            int lo = 0, hi = nblk - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.item0 + rows_prefix(a, p.s, ti, mid) <= at) lo = mid; else hi = mid - 1;
+            }
+            p.qb = lo;
+            p.item0 += rows_prefix(a, p.s, ti, lo);
+        } else {
+            for (;; ++p.qb) {
+                const int t = rows_block_tiles(a, p.s, ti, p.qb);
+                if (at < p.item0 + t) break;
+                p.item0 += t;
+            }
+        }
+        if (inside) bound = rows_block_tiles(a, p.s, ti, p.qb) <= a.split_min ? p.item0 : at;
+    }
+    begin = __shfl_sync(FULL, bound, 0);
+    end = __shfl_sync(FULL, bound, 1);
+    place.b = __shfl_sync(FULL, p.b, 0);
+    place.kv = __shfl_sync(FULL, p.kv, 0);
+    place.qb = __shfl_sync(FULL, p.qb, 0);
+    place.item0 = __shfl_sync(FULL, p.item0, 0);
+    if (begin < end) place.s = rows_seq(a, place.b);
 }
 
 __device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
@@ -241,6 +271,11 @@ __device__ __forceinline__ void rows_tmem_st16(uint32_t taddr, const uint32_t (&
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+
+// Folded items take the tiles in the order K_0 K_1 V_0 K_2 V_1 ... V_(n-2) V_(n-1),
+// the others K_0 V_0 K_1 V_1 ...: places of tile j's K and V among the item's 2 n.
+__device__ __forceinline__ int rows_k_place(bool fold, int j) { return fold && j > 0 ? 2 * j - 1 : 2 * j; }
+__device__ __forceinline__ int rows_v_place(bool fold, int j, int n) { return fold ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1; }
 
 // One bit per score column of a tile: the keys [0, lim) of 128.
 __device__ __forceinline__ uint32_t lead_word(int lim, int k) {
@@ -280,6 +315,17 @@ __device__ __forceinline__ uint4 finite_only(uint4 v) {
     return v;
 }
 
+// Shared-memory descriptors (kvc_tcgen05.cuh) with the 128-byte swizzle in two
+// halves: the start address (and leading offset), and the rest.
+__host__ __device__ constexpr uint32_t rows_desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint64_t rows_desc(uint32_t lo, uint32_t hi) { return (uint64_t(hi) << 32) | lo; }
+
+__device__ __forceinline__ bool rows_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs a) {
     using C = RowsTcCfg<D>;
@@ -297,13 +343,20 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     const uint32_t ring = sb + C::RING_OFF;
     const uint32_t full = sb + C::BAR_OFF, empty = full + 8 * NS, s_full = empty + 8 * NS, p_full = s_full + 16,
                    o_full = p_full + 16, o_free = o_full + 16, q_full = o_free + 16, q_empty = q_full + 8,
-                   item_full = q_empty + 8, item_empty = item_full + 16, mma_done = item_empty + 16;
+                   item_full = q_empty + 8, item_empty = item_full + 16, fold_bar = item_empty + 16, mma_done = fold_bar + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::NBAR);
     volatile int *flags = reinterpret_cast<volatile int *>(smem + C::BAR_OFF + 8 * C::NBAR + 8);  // abort, then odd[4]
     volatile int *odd = flags + 1;  // item i met infinities or NaN: odd[i % 4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group, TB = 128 / G, TI = 2 * TB;
 
+    if (threadIdx.x == 32) {
+        dev::prefetch_tensormap(&a.tm_q);
+        dev::prefetch_tensormap(&a.tm_k);
+        dev::prefetch_tensormap(&a.tm_v);
+        dev::prefetch_tensormap(&a.tm_k_new);
+        dev::prefetch_tensormap(&a.tm_v_new);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             dev::mbar_init(full + 8 * s, 1);
@@ -313,12 +366,13 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             dev::mbar_init(s_full + 8 * x, 1);       // S_x is in tensor memory, PV_x before it done
             dev::mbar_init(p_full + 8 * x, 4);       // the four softmax warps wrote P_x
             dev::mbar_init(o_full + 8 * x, 1);       // the item's last PV_x is done
-            dev::mbar_init(o_free + 8 * x, 4);       // its accumulator is read
+            dev::mbar_init(o_free + 8 * x, 4);       // its accumulator is read (folded items: by stream B's warps)
             dev::mbar_init(item_full + 8 * x, 1);
-            dev::mbar_init(item_empty + 8 * x, 11);  // every role but the item warp has read the item (the second query warp too)
+            dev::mbar_init(item_empty + 8 * x, 10);  // every other warp has read the item
         }
-        dev::mbar_init(q_full, 2);    // both query warps
+        dev::mbar_init(q_full, 1);
         dev::mbar_init(q_empty, 1);   // the item's last S has read Q
+        dev::mbar_init(fold_bar, 4);  // stream A's (max, sum) are in shared memory
         dev::mbar_init(mma_done, 1);
         for (int i = 0; i < 5; ++i) flags[i] = 0;
         dev::fence_mbar_init();
@@ -347,40 +401,15 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         it = *reinterpret_cast<const RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1));
         return true;
     };
-    // one query tile's rows of an item into its Q buffer, by one warp
-    auto copy_q = [&](const RowsItem &it, int x) {
-        const int nt = min(TB, it.ntok - x * TB);
-        if (nt <= 0) return;
-        const int H = a.H_kv * G;
-        RowsSeq s;
-        s.row0 = it.row0;
-        const uint32_t qt = sb + x * C::TILE_BYTES;
-        const int total = G * nt * C::CHUNKS;
-        for (int i = lane; i < total; i += 32) {
-            const int c16 = i % C::CHUNKS, rr = i / C::CHUNKS, head = rr / nt, tt = rr - head * nt;
-            const T *src = reinterpret_cast<const T *>(a.q) + rows_offset(a, s, it.b, H, it.kv * G + head, it.t0 + x * TB + tt, D);
-            dev::cp_async_16(C::swz(qt, head * TB + tt, c16), reinterpret_cast<const uint4 *>(src) + c16);
-        }
-        cp_async_wait_all();
-        dev::fence_proxy_async_smem();
-    };
-
-    int issued = 0;  // stages filled by the copy warp
+    int issued = 0, queries = 0;  // stages filled by the copy warp, items whose queries were copied
     if (warp == C::ITEM_WARP) {
-        // ------------------------------------------------------------ items, and Q of tile A
-        if (blockIdx.x == 0)  // sequences whose arguments are out of range
-            for (int i = lane; i < a.B; i += 32)
-                if (rows_seq(a, i).bad) dev::record_error(a.err, ERR_DEVICE_INDEX);
-        RowsWalk w;
-        w.total_of(a, TI, lane);
-        const int grid = int(gridDim.x), me = int(blockIdx.x);
-        int64_t share = (w.total + grid - 1) / grid;
-        if (share < a.min_share) share = a.min_share;
-        const int64_t end = rows_boundary(a, w, TI, lane, share, me + 1);
-        const int64_t begin = rows_boundary(a, w, TI, lane, share, me);
+        // ------------------------------------------------------------ items and their queries
+        int64_t share, begin, end;
+        RowsPlace w;
+        rows_plan(a, TI, lane, share, begin, end, w);
+        const int me = int(blockIdx.x);
         RowsCut cut = {0, 0, 0, 0, 0};
         bool ok = true;
-        if (begin < end) w.locate(a, TI, lane, begin);
         int64_t at = begin;
         for (int k = 0; ok; ++k) {
             RowsItem it;
@@ -402,9 +431,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 // one that goes on with it the first
                 it.slot = it.j0 == 0 && it.j1 == tiles ? -1 : 2 * me + (it.j0 == 0 ? 1 : 0);
                 if (it.j0 == 0 && it.j1 < tiles)
-                    cut = {int((w.item0 + tiles - 1) / share) - me + 1, it.b, it.kv, it.t0, it.ntok};
+                    cut = {int(rows_div(w.item0 + tiles - 1, share)) - me + 1, it.b, it.kv, it.t0, it.ntok};
                 at = w.item0 + it.j1;
-                if (at < end) w.next(a, TI);
             }
             if (k >= 2) ok = __all_sync(FULL, dev::mbar_wait_bounded(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
             if (!ok) break;
@@ -415,28 +443,28 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (it.b < 0) break;
             if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
             if (!ok) break;
-            copy_q(it, 0);
+            if (lane == 0) {
+                // one box of TB tokens x g heads per column block and query tile
+                const int nx = it.ntok > TB ? 2 : 1;
+                dev::mbar_arrive_expect_tx(q_full, uint32_t(nx * CB * G * TB) * 128);
+                for (int x = 0; x < nx; ++x)
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) {
+                        const uint32_t dst = sb + x * C::TILE_BYTES + cb * BLK;
+                        if (a.cu_seqlens)
+                            dev::tma_load_3d(dst, &a.tm_q, cb * 64, it.kv * G, it.row0 + it.t0 + x * TB, q_full);
+                        else
+                            dev::tma_load_4d(dst, &a.tm_q, cb * 64, it.kv * G, it.t0 + x * TB, it.b, q_full);
+                    }
+            }
+            queries = k + 1;
             __syncwarp();
-            if (lane == 0) dev::mbar_arrive(q_full);
+            if (at < end) w.next(a, TI);
         }
         if (lane == 0) a.cuts[me] = cut;
-        if (!ok) give_up();
-    } else if (warp == C::Q_WARP) {
-        // ------------------------------------------------------------ Q of tile B
-        bool ok = true;
-        RowsItem it;
-        for (int k = 0; ok; ++k) {
-            ok = __all_sync(FULL, take_item(k, it));
-            __syncwarp();
-            if (!ok) break;
-            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
-            if (it.b < 0) break;
-            if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
-            if (!ok) break;
-            copy_q(it, 1);
-            __syncwarp();
-            if (lane == 0) dev::mbar_arrive(q_full);
-        }
+        if (me == 0)  // sequences whose arguments are out of range
+            for (int i = lane; i < a.B; i += 32)
+                if (rows_seq(a, i).bad) dev::record_error(a.err, ERR_DEVICE_INDEX);
         if (!ok) give_up();
     } else if (warp == C::K_WARP) {
         // ------------------------------------------------------------ K and V copies
@@ -448,18 +476,22 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (!ok) break;
             if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
             if (it.b < 0) break;
+            const int n = it.j1 - it.j0;
+            const bool fold = it.ntok <= TB && n > 1;
+            // the tile at place i, and whether it is V
+            auto tile_at = [&](int i) { return it.j0 + (fold ? (i == 2 * n - 1 ? n - 1 : i & 1 ? (i + 1) >> 1 : i ? (i >> 1) - 1 : 0) : i >> 1); };
             // a page's number is looked up a tile ahead
-            auto page_of = [&](int j) {
-                const int blk = 8 * j + lane;
-                if (!a.block_table || lane >= 8 || j >= min(it.np, it.j1) || blk * 16 >= it.c) return 0;
-                return __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk);
+            auto page_at = [&](int i) {
+                if (!a.block_table || lane >= 8 || i >= 2 * n) return 0;
+                const int j = tile_at(i), blk = 8 * j + lane;
+                return j < it.np && blk * 16 < it.c ? __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk) : 0;
             };
-            int next_page = page_of(it.j0);
-            for (int j = it.j0; ok && j < it.j1; ++j) {
-                const int page = next_page;
-                next_page = page_of(j + 1);
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
+            int next_page = page_at(0);
+            for (int i = 0; i < 2 * n; ++i) {
+                const int page = next_page, j = tile_at(i);
+                const bool v = fold ? i > 0 && (i == 2 * n - 1 || !(i & 1)) : i & 1;
+                next_page = page_at(i + 1);
+                {
                     const int s = issued % NS;
                     if (issued >= NS)
                         ok = __all_sync(FULL, dev::mbar_wait_bounded(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
@@ -505,99 +537,118 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         if (!ok) give_up();
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
-            bool ok = true;
-            RowsItem it;
-            uint32_t st = 0;           // stages consumed so far
-            uint32_t tiles[2] = {0, 0}, items[2] = {0, 0};  // of each query tile
-            auto stage_wait = [&](uint32_t i) { return dev::mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, flags, a.timeout_ns); };
-            auto issue_s = [&](int x, uint32_t i, bool paged) {
-                const uint32_t kt = ring + (i % NS) * C::TILE_BYTES, qt = sb + x * C::TILE_BYTES, s_t = tmem + C::S_COL + 128 * x;
+        // The whole warp walks the loop, one elected lane issues: the operands'
+        // descriptors then stay warp-uniform, and each is its tile's plus a constant.
+        const bool leader = rows_elect();
+        constexpr uint32_t HI1 = rows_desc_hi(1024), HI4 = rows_desc_hi(4096);
+        bool ok = true;
+        RowsItem it;
+        uint32_t st = 0;                                // places consumed so far
+        uint32_t tiles[2] = {0, 0}, items[2] = {0, 0};  // of each stream
+        auto stage_wait = [&](uint32_t i) { return dev::mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, flags, a.timeout_ns); };
+        auto issue_s = [&](int x, int qx, uint32_t i, bool paged) {
+            const uint32_t kt = (ring + (i % NS) * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
+            if (leader) {
                 if (CB == 2 && paged) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
-                            tc::mma_f16_ss(s_t + 64 * h, tc::smem_desc_sw128(qt + (ks >> 2) * BLK + (ks & 3) * 32, 16, 1024),
-                                           tc::smem_desc_sw128(kt + (ks >> 2) * 2048 + (ks & 3) * 32 + h * 1024, 16, 4096), IDESC_S64, ks > 0);
+                            tc::mma_f16_ss(s_t + 64 * h, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
+                                           rows_desc(kt + (((ks >> 2) * 2048 + (ks & 3) * 32 + h * 1024) >> 4), HI4), IDESC_S64, ks > 0);
                 } else {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        tc::mma_f16_ss(s_t, tc::smem_desc_sw128(qt + (ks >> 2) * BLK + (ks & 3) * 32, 16, 1024),
-                                       tc::smem_desc_sw128(kt + (ks >> 2) * BLK + (ks & 3) * 32, 16, 1024), IDESC_S, ks > 0);
+                        tc::mma_f16_ss(s_t, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
+                                       rows_desc(kt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1), IDESC_S, ks > 0);
                 }
                 tc::commit(s_full + 8 * x);
-            };
-            auto issue_pv = [&](int x, uint32_t i, bool paged, bool first) {
-                const uint32_t vt = ring + (i % NS) * C::TILE_BYTES, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
+            }
+        };
+        auto issue_pv = [&](int x, uint32_t i, bool paged, bool first) {
+            const uint32_t vt = (ring + (i % NS) * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
+            if (leader) {
+                if (CB == 2 && paged) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint64_t desc = CB == 2 && paged ? tc::smem_desc_sw128(vt + (ks & 3) * 8192 + (ks >> 2) * 1024, 2048, 4096)
-                                                           : tc::smem_desc_sw128(vt + ks * 2048, BLK, 1024);
-                    tc::mma_f16_ts(o_t, p_t + 8 * ks, desc, IDESC_O, !first || ks > 0);
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + (((ks & 3) * 8192 + (ks >> 2) * 1024) >> 4) + ((2048 >> 4) << 16), HI4),
+                                       IDESC_O, ks > 0 || !first);
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 2048) >> 4) + ((BLK >> 4) << 16), HI1), IDESC_O, ks > 0 || !first);
                 }
-            };
-            for (int k = 0; ok; ++k) {
-                ok = take_item(k, it);
+            }
+        };
+        auto commit_to = [&](uint32_t bar) {
+            if (leader) tc::commit(bar);
+        };
+        for (int k = 0; ok; ++k) {
+            ok = __all_sync(FULL, take_item(k, it));
+            __syncwarp();
+            if (!ok) break;
+            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+            if (it.b < 0) break;
+            const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
+            const bool fold = nx == 1 && n > 1;
+            auto is_paged = [&](int j) { return a.block_table && it.j0 + j < it.np; };
+            ok = dev::mbar_wait_bounded(q_full, uint32_t(k) & 1, flags, a.timeout_ns) && stage_wait(st);
+            if (fold) ok = ok && stage_wait(st + 1);
+            ok = __all_sync(FULL, ok);
+            if (!ok) break;
+            tc::fence_after();
+            issue_s(0, 0, st, is_paged(0));
+            if (fold) commit_to(empty + 8 * (st % NS));
+            if (fold || nx == 2) issue_s(1, fold ? 0 : 1, fold ? st + 1 : st, is_paged(fold ? 1 : 0));
+            commit_to(empty + 8 * ((fold ? st + 1 : st) % NS));
+            if (n == (fold ? 2 : 1)) commit_to(q_empty);
+            const int steps = fold ? n : n * nx;
+            for (int u = 0; u < steps; ++u) {
+                const int x = fold || nx == 2 ? u & 1 : 0, j = fold || nx == 1 ? u : u >> 1;
+                const int jn = fold ? j + 2 : j + 1;
+                const bool first = fold ? j < 2 : j == 0, release = fold || x == nx - 1;
+                const uint32_t sv = st + rows_v_place(fold, j, n);
+                ok = dev::mbar_wait_bounded(p_full + 8 * x, tiles[x] & 1, flags, a.timeout_ns) && stage_wait(sv);
+                if (ok && first && items[x] > 0) ok = dev::mbar_wait_bounded(o_free + 8 * x, (items[x] - 1) & 1, flags, a.timeout_ns);
+                ok = __all_sync(FULL, ok);
                 if (!ok) break;
-                dev::mbar_arrive(item_empty + 8 * (k & 1));
-                if (it.b < 0) break;
-                const int nx = it.ntok > TB ? 2 : 1, n = it.j1 - it.j0;
-                auto is_paged = [&](int j) { return a.block_table && it.j0 + j < it.np; };
-                ok = dev::mbar_wait_bounded(q_full, uint32_t(k) & 1, flags, a.timeout_ns) && stage_wait(st);
-                if (!ok) break;
+                ++tiles[x];
                 tc::fence_after();
-                for (int x = 0; x < nx; ++x) issue_s(x, st, is_paged(0));
-                tc::commit(empty + 8 * (st % NS));
-                if (n == 1) tc::commit(q_empty);
-                for (int j = 0; ok && j < n; ++j) {
-                    const uint32_t sv = st + 2 * j + 1, sk = sv + 1;
-                    for (int x = 0; x < nx; ++x) {
-                        ok = dev::mbar_wait_bounded(p_full + 8 * x, tiles[x] & 1, flags, a.timeout_ns);
-                        if (ok && x == 0) ok = stage_wait(sv);
-                        if (ok && j == 0 && items[x] > 0) ok = dev::mbar_wait_bounded(o_free + 8 * x, (items[x] - 1) & 1, flags, a.timeout_ns);
-                        if (!ok) break;
-                        ++tiles[x];
-                        tc::fence_after();
-                        issue_pv(x, sv, is_paged(j), j == 0);
-                        if (x == nx - 1) tc::commit(empty + 8 * (sv % NS));
-                        if (j + 1 < n) {
-                            if (x == 0) ok = stage_wait(sk);
-                            if (!ok) break;
-                            tc::fence_after();
-                            issue_s(x, sk, is_paged(j + 1));
-                            if (x == nx - 1) {
-                                tc::commit(empty + 8 * (sk % NS));
-                                if (j + 2 == n) tc::commit(q_empty);
-                            }
-                        } else {
-                            tc::commit(o_full + 8 * x);
-                            ++items[x];
-                        }
+                issue_pv(x, sv, is_paged(j), first);
+                if (release) commit_to(empty + 8 * (sv % NS));
+                if (jn < n) {
+                    const uint32_t sk = st + rows_k_place(fold, jn);
+                    ok = __all_sync(FULL, stage_wait(sk));
+                    if (!ok) break;
+                    tc::fence_after();
+                    issue_s(x, fold ? 0 : x, sk, is_paged(jn));
+                    if (release) {
+                        commit_to(empty + 8 * (sk % NS));
+                        if (jn == n - 1) commit_to(q_empty);
                     }
+                } else {
+                    commit_to(o_full + 8 * x);
+                    ++items[x];
                 }
-                st += 2 * n;
             }
-            if (!ok) {
-                if (!flags[0]) dev::record_error(a.err, ERR_TIMEOUT);
-                flags[0] = 1;
-            }
-            tc::commit(mma_done);  // every MMA is done before tensor memory is freed
-            const volatile int never = 0;
-            dev::mbar_wait_bounded(mma_done, 0, &never, a.timeout_ns);
+            st += 2 * n;
         }
+        if (!ok) give_up();
+        commit_to(mma_done);  // every MMA is done before tensor memory is freed
+        const volatile int never = 0;
+        dev::mbar_wait_bounded(mma_done, 0, &never, a.timeout_ns);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
         const int x = warp >> 2, qd = warp & 3;
         const int r = 32 * qd + lane;           // query row = TMEM lane
-        const int head = r / TB, tt = r - head * TB;
+        const int tt = r / G, head = r - tt * G;
         const int H = a.H_kv * G;
         const uint32_t lane_base = uint32_t(qd * 32) << 16;
         const uint32_t s_t = tmem + lane_base + C::S_COL + 128 * x, o_t = tmem + lane_base + C::O_COL + D * x;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
         bool ok = true;
-        uint32_t st = 0, gt = 0, gi = 0;  // ring position; tiles and items of this query tile so far
+        uint32_t st = 0, gt = 0, gi = 0, folds = 0;  // ring position; tiles, items and folded items of this stream so far
         RowsItem it;
         for (int k = 0; ok; ++k) {
             ok = __all_sync(FULL, take_item(k, it));
@@ -606,60 +657,68 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
             if (it.b < 0) break;
             const int n = it.j1 - it.j0;
-            if (x == 1 && it.ntok <= TB) {  // one query tile only
+            const bool two = it.ntok > TB, fold = !two && n > 1;
+            if (x == 1 && !two && !fold) {  // nothing for stream B
                 st += 2 * n;
                 continue;
             }
+            const int qx = two ? x : 0;  // query tile of this stream
             // (the slot of item k - 3, which every role has left: it has taken item k - 2)
             if (threadIdx.x == 0) odd[(k + 1) & 3] = 0;
-            const int t = it.t0 + x * TB + tt;              // token
-            const bool row_ok = head < G && x * TB + tt < it.ntok;
+            const int t = it.t0 + qx * TB + tt;              // token
+            const bool row_ok = tt < TB && qx * TB + tt < it.ntok;
+            const bool warp_ok = __any_sync(FULL, row_ok);  // else the warp's lanes hold no query row
             float m_run = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
-            for (int j = 0; j < n; ++j, ++gt) {
-                ok = __all_sync(FULL, !flags[0] && dev::mbar_wait_bounded(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
+            const int j_first = fold ? x : 0;
+            for (int j = j_first; j < n; j += fold ? 2 : 1, ++gt) {
+                ok = __all_sync(FULL, dev::mbar_wait_bounded(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
                 if (!ok) break;
                 tc::fence_after();
+                // the V rows that a partly visible tile has to be rid of (below)
+                const int jt = it.j0 + j;
+                const bool is_new = jt >= it.np;
+                const int key0 = 128 * (is_new ? jt - it.np : jt);         // first key, among the cached or the new rows
+                const int nv = min(128, (is_new ? it.vis : it.c) - key0);  // the tile's own rows
+                // does every row of the item see the whole tile?
+                const bool partial = nv < 128 || (is_new && (a.tree_mask || key0 + 127 > it.t0));
+                if (partial && (x == 0 || fold)) {
+                    // V rows behind the tile's own are zeroed, infinities and NaN of
+                    // rows that not everybody sees set aside (with two query tiles
+                    // PV_B follows PV_A, which waits for these warps)
+                    const uint32_t sv = st + rows_v_place(fold, j, n);
+                    ok = __all_sync(FULL, dev::mbar_wait_bounded(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns));
+                    if (!ok) break;
+                    const uint32_t vt = ring + (sv % NS) * C::TILE_BYTES;
+                    const bool paged = a.block_table && !is_new;
+                    for (int i = is_new ? r : r + nv * C::CHUNKS; i < 128 * C::CHUNKS; i += 128) {
+                        const int row = i / C::CHUNKS, c16 = i % C::CHUNKS;
+                        const uint32_t at = paged ? C::swz_paged(vt, row, c16) : C::swz(vt, row, c16);
+                        if (row >= nv) {
+                            dev::st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
+                        } else {
+                            uint4 v;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+                            if (not_finite<T>(v)) {
+                                odd[k & 3] = 1;
+                                dev::st_shared_v4(at, finite_only<T>(v));
+                            }
+                        }
+                    }
+                    dev::fence_proxy_async_smem();
+                }
+                if (!warp_ok) {
+                    __syncwarp();
+                    if (lane == 0) dev::mbar_arrive(p_full + 8 * x);
+                    continue;
+                }
                 uint32_t sr[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32(s_t + 32 * q, sr[q]);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::reg_fence(sr[q]);
-                // ---- the keys of the tile that this row sees
-                const int jt = it.j0 + j;
-                const bool is_new = jt >= it.np;
-                const int key0 = 128 * (is_new ? jt - it.np : jt);       // first key, among the cached or the new rows
-                const int nv = min(128, (is_new ? it.vis : it.c) - key0);  // the tile's own rows
-                // does every row of the item see the whole tile?
-                const bool partial = nv < 128 || (is_new && (a.tree_mask || key0 + 127 > it.t0));
-                if (partial) {
-                    if (x == 0 && (nv < 128 || is_new)) {
-                        // V rows behind the tile's own are zeroed, infinities and NaN of
-                        // rows that not everybody sees set aside (PV_B follows PV_A, which
-                        // waits for these warps)
-                        const uint32_t sv = st + 2 * j + 1;
-                        ok = __all_sync(FULL, dev::mbar_wait_bounded(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns));
-                        if (!ok) break;
-                        const uint32_t vt = ring + (sv % NS) * C::TILE_BYTES;
-                        const bool paged = a.block_table && !is_new;
-#pragma unroll 1
-                        for (int i = r; i < 128 * C::CHUNKS; i += 128) {
-                            const int row = i / C::CHUNKS, c16 = i % C::CHUNKS;
-                            const uint32_t at = paged ? C::swz_paged(vt, row, c16) : C::swz(vt, row, c16);
-                            if (row >= nv) {
-                                dev::st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
-                            } else if (is_new) {
-                                uint4 v;
-                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-                                if (not_finite<T>(v)) {
-                                    odd[k & 3] = 1;
-                                    dev::st_shared_v4(at, finite_only<T>(v));
-                                }
-                            }
-                        }
-                        dev::fence_proxy_async_smem();
-                    }
+                if (partial) {  // the keys of the tile that this row sees
                     uint32_t w[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -691,7 +750,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 m_run = m_new;
                 const float negm = m_run == -INFINITY ? 0.f : -m_run;
                 const float2 neg2 = make_float2(negm, negm);
-                if (j > 0 && __any_sync(FULL, corr != 1.f)) {
+                if (j > j_first && __any_sync(FULL, corr != 1.f)) {
                     // PV of the tile before is done (it precedes this S), the next waits for P
                     const float2 c2 = make_float2(corr, corr);
 #pragma unroll 1
@@ -732,12 +791,38 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (!ok) break;
             st += 2 * n;
             // ---- epilogue
-            ok = __all_sync(FULL, !flags[0] && dev::mbar_wait_bounded(o_full + 8 * x, gi & 1, flags, a.timeout_ns));
+            float l = l2.x + l2.y, f_a = 0.f, f_b = 1.f;  // folded items: factors of the two accumulators
+            float2 *fold_ml = reinterpret_cast<float2 *>(smem + C::FOLD_OFF);
+            if (fold && x == 0) {
+                // stream B reads both accumulators (and lets them go; those of the
+                // item before, too, before its values here are overwritten)
+                ok = k == 0 || __all_sync(FULL, dev::mbar_wait_bounded(o_free, uint32_t(k - 1) & 1, flags, a.timeout_ns));
+                if (!ok) break;
+                fold_ml[r] = make_float2(m_run, l);
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(fold_bar);
+                ++gi;
+                continue;
+            }
+            ok = dev::mbar_wait_bounded(o_full + 8 * x, gi & 1, flags, a.timeout_ns);
+            if (fold) {  // (stream A has a part in every item: its phase is k's)
+                ok = ok && dev::mbar_wait_bounded(fold_bar, folds & 1, flags, a.timeout_ns) &&
+                     dev::mbar_wait_bounded(o_full, uint32_t(k) & 1, flags, a.timeout_ns);
+                ++folds;
+            }
+            ok = __all_sync(FULL, ok);
             if (!ok) break;
             ++gi;
             tc::fence_after();
+            if (fold) {
+                const float2 ml = fold_ml[r];
+                const float M = fmaxf(m_run, ml.x);
+                f_a = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                f_b = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
+                l = l * f_b + ml.y * f_a;
+                m_run = M;
+            }
             const bool any_odd = odd[k & 3] != 0;
-            const float l = l2.x + l2.y;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             RowsSeq sq;
             sq.row0 = it.row0;
@@ -747,7 +832,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 if (it.slot < 0) {
                     orow = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + head, t, D));
                 } else {
-                    const int64_t row = int64_t(it.slot) * 256 + 128 * x + r;
+                    const int64_t row = int64_t(it.slot) * 256 + 128 * qx + r;
                     prow = a.part_acc + row * D;
                     *reinterpret_cast<float2 *>(a.part_ml + 2 * row) = make_float2(m_run, l);
                 }
@@ -756,12 +841,26 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tc::tmem_ld32(o_t + 32 * q, o);
-                tc::tmem_ld_wait();
-                tc::reg_fence(o);
-                if (q == D / 32 - 1) {  // the accumulator is read: the next item's PV may overwrite it
+                if (fold) {
+                    uint32_t oa[32];
+                    tc::tmem_ld32(o_t - D + 32 * q, oa);
+                    tc::tmem_ld_wait();
+                    tc::reg_fence(oa);
+                    tc::reg_fence(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f_b, __uint_as_float(oa[e]) * f_a));
+                } else {
+                    tc::tmem_ld_wait();
+                    tc::reg_fence(o);
+                }
+                if (q == D / 32 - 1) {  // the accumulators are read: the next item's PV may overwrite them
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) dev::mbar_arrive(o_free + 8 * x);
+                    if (lane == 0) {
+                        dev::mbar_arrive(o_free + 8 * x);
+                        if (fold) dev::mbar_arrive(o_free);
+                    }
                 }
                 if (any_odd && row_ok) {
                     // infinities and NaN among the V rows that this row sees (of
@@ -808,8 +907,12 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         tc::fence_after();
         tc::tmem_dealloc(tmem, C::TMEM_COLS);
     }
+    // after an abort, wait (bounded) for the copies that may still land
+    if (warp == C::ITEM_WARP && lane == 0 && flags[0] && queries > 0) {
+        const volatile int never = 0;
+        dev::mbar_wait_bounded(q_full, uint32_t(queries - 1) & 1, &never, a.timeout_ns);
+    }
     if (warp == C::K_WARP && lane == 0 && flags[0]) {
-        // after an abort, wait (bounded) for the copies that may still land
         const volatile int never = 0;
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
             dev::mbar_wait_bounded(full + 8 * (i % NS), uint32_t(i / NS) & 1, &never, a.timeout_ns);
@@ -831,7 +934,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
     const int nt = blockIdx.y * 8 + warp;   // row of the item: (token, head)
     if (nt >= cut.ntok * G) return;
     const int tok = nt / G, head = nt - tok * G, x = tok / TB;
-    const int r = 128 * x + head * TB + (tok - x * TB);
+    const int r = 128 * x + (tok - x * TB) * G + head;
     auto row_of = [&](int p) { return int64_t(p == 0 ? 2 * i + 1 : 2 * (i + p)) * 256 + r; };
     float M = -INFINITY;
     for (int p = lane; p < cut.pieces; p += 32) M = fmaxf(M, __ldcg(a.part_ml + 2 * row_of(p)));
