@@ -391,7 +391,8 @@ uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
  *   out          device, [total, H, d_h], 16-byte aligned
  * Paged handles: a block-table entry outside [0, num_blocks) among a
  * sequence's cached rows records KVC_ERR_DEVICE_INDEX; that sequence's output
- * is then undefined.
+ * is then undefined.  KVC_ERR_UNSUPPORTED also for a call whose product of
+ * query blocks and key tiles passes 2^31 (over a million packed tokens).
  * Host errors: KVC_ERR_INVALID, KVC_ERR_UNSUPPORTED, KVC_ERR_ALIGNMENT,
  * KVC_ERR_WORKSPACE, KVC_ERR_CUDA. */
 kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const void *k, const void *v,

@@ -76,8 +76,9 @@ constexpr int ROWS_MAX_CTAS = 160;  // sizes the workspace
 struct RowsTcArgs : RowsArgs {
     RowsCut *cuts;               // [grid]
     float *part_ml;              // [2 grid][256][2]: (max, sum) of a piece's query rows
-    float *part_acc;             // [2 grid][256][D]: their unnormalised accumulators
-    int32_t min_share;           // key tiles of a CTA's share, at least
+    float *part_acc;             // [2 grid][D / 4][256][4]: their unnormalised accumulators
+    int32_t item_cost;           // an item's start and end, in key tiles
+    int32_t min_share;           // length of a CTA's share of the line, at least
     int32_t split_min;           // items of at most so many key tiles are not cut
     int32_t seg_base;            // tensor-map segment (block) of the layer's first: layer * B * H_kv (layer * num_blocks)
     int32_t pool_end;            // paged: one past the map's last block

@@ -89,17 +89,20 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     a.cuts = reinterpret_cast<kvc::RowsCut *>(ws);
     a.part_ml = reinterpret_cast<float *>(ws + ml);
     a.part_acc = reinterpret_cast<float *>(ws + acc);
-    // at most so many key tiles: of one item, and of all
+    // at most so many key tiles of one item, and length of the whole line
     const int ti = 2 * (128 / h->group);
     const int64_t item = (max_cached + 127) / 128 + (int64_t(max_tokens) + 127) / 128;
-    a.min_share = 4;
-    a.split_min = item > 4 ? 4 : 0x7fffffff;  // (nothing is cut where no combine follows)
     const int64_t blocks = r.cu_seqlens ? r.total / ti + (c.batch < r.total ? c.batch : r.total)
                                         : int64_t(c.batch) * ((r.T + ti - 1) / ti);
-    const int64_t want = (blocks * c.n_kv_heads * item + a.min_share - 1) / a.min_share;
+    a.item_cost = 2;
+    a.min_share = 4 + a.item_cost;
+    a.split_min = item > 4 ? 4 : 0x7fffffff;  // (nothing is cut where no combine follows)
+    const int64_t line = blocks * c.n_kv_heads * (item + a.item_cost);
+    if (line > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     int64_t grid = h->num_sms < kvc::ROWS_MAX_CTAS ? h->num_sms : kvc::ROWS_MAX_CTAS;
-    if (want < grid) grid = want;
-    const int rows = (max_tokens < ti ? max_tokens : ti) * h->group;
+    if ((line + a.min_share - 1) / a.min_share < grid) grid = (line + a.min_share - 1) / a.min_share;
+    // the query tiles an item can fill
+    const int rows = max_tokens >= ti ? 256 : max_tokens > ti / 2 ? 128 + (max_tokens - ti / 2) * h->group : max_tokens * h->group;
     const cudaError_t e = h->rows->launch(a, int(grid), item > 4 ? rows : 0, s);
     return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }

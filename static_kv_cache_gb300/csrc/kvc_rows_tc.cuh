@@ -83,7 +83,10 @@ struct RowsTcCfg {
     static constexpr int FOLD_OFF = ITEM_OFF + 2 * 64;            // folded items: stream A's (max, sum) of each row
     static constexpr int SMEM = 1024 + FOLD_OFF + 128 * 8;
     static constexpr int K_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10;
-    static constexpr int THREADS = 11 * 32;
+    static constexpr int THREADS = 12 * 32;  // (the last warp only fills its warpgroup)
+    // registers: 168 a thread at launch; the softmax warpgroups take from the third
+    static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
+    static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * 168, "the launch's registers");
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // S_A, S_B (128 columns each), O_A, O_B (D each)
     static constexpr float RESCALE_LOG2 = 8.f;
@@ -114,26 +117,28 @@ static_assert(sizeof(RowsItem) <= 64, "item slot");
 
 // ---- the line of key tiles ------------------------------------------------------
 
-// Key tiles of the first q token blocks (of ti tokens) of one KV head of a
-// sequence: every block's cached tiles, and the new tiles its rows can see --
-// all of them under a mask, those up to its last token otherwise.
-__device__ __forceinline__ int64_t rows_prefix(const RowsArgs &a, const RowsSeq &s, int ti, int q) {
-    const int64_t np = (s.c + 127) / 128, kt = (s.n + 127) / 128;
-    if (a.tree_mask) return q * (np + kt);
-    const int nblk = (s.n + ti - 1) / ti;
-    if (ti > 128)  // 256 tokens: block k (from 1) sees 2 k tiles, the last one kt
-        return q * np + (q < nblk ? int64_t(q) * (q + 1) : int64_t(nblk) * (nblk - 1) + kt);
+// Length on the line of the first q token blocks (of ti tokens) of one KV head
+// of a sequence: a.item_cost each for an item's start and end, and its key
+// tiles -- the cached ones, and of the new ones all under a mask, otherwise
+// those up to its last token.  (The host keeps the whole line below 2^31.)
+__device__ __forceinline__ int rows_prefix(const RowsTcArgs &a, const RowsSeq &s, int ti, int q) {
+    const int base = q * (a.item_cost + (s.c + 127) / 128), kt = (s.n + 127) / 128;
+    if (a.tree_mask) return base + q * kt;
+    if (ti > 128) {  // 256 tokens: block k (from 1) sees 2 k tiles, the last one kt
+        const int nblk = (s.n + ti - 1) / ti;
+        return base + (q < nblk ? q * (q + 1) : nblk * (nblk - 1) + kt);
+    }
     const int m = 128 / ti;
     if (m * ti == 128) {  // m blocks a tile
-        const int64_t full = q / m, rest = q - full * m;
-        return q * np + m * full * (full + 1) / 2 + rest * (full + 1);
+        const int full = q / m, rest = q - full * m;
+        return base + m * full * (full + 1) / 2 + rest * (full + 1);
     }
-    int64_t sum = q * np;
+    int sum = base;
     for (int k = 1; k <= q; ++k) sum += (min(s.n, k * ti) + 127) / 128;
     return sum;
 }
 
-__device__ __forceinline__ int64_t rows_seq_tiles(const RowsArgs &a, const RowsSeq &s, int ti) {
+__device__ __forceinline__ int rows_seq_length(const RowsTcArgs &a, const RowsSeq &s, int ti) {
     return s.n == 0 ? 0 : rows_prefix(a, s, ti, (s.n + ti - 1) / ti);
 }
 
@@ -142,20 +147,13 @@ __device__ __forceinline__ int rows_block_tiles(const RowsArgs &a, const RowsSeq
     return (s.c + 127) / 128 + (end + 127) / 128;
 }
 
-// 64-bit quotient; the values fit 32 bits but for enormous calls.
-__device__ __forceinline__ int64_t rows_div(int64_t x, int64_t y) {
-    return (uint64_t(x) | uint64_t(y)) >> 32 ? x / y : int64_t(uint32_t(x) / uint32_t(y));
-}
-
-// A place on the line: token block qb of (b, kv), whose key tiles start at
-// item0.
+// A place on the line: token block qb of (b, kv), an item that starts at item0.
 struct RowsPlace {
-    int b, kv, qb;
-    int64_t item0;
+    int b, kv, qb, item0;
     RowsSeq s;
 
-    __device__ __forceinline__ void next(const RowsArgs &a, int ti) {
-        item0 += rows_block_tiles(a, s, ti, qb);
+    __device__ __forceinline__ void next(const RowsTcArgs &a, int ti) {
+        item0 += a.item_cost + rows_block_tiles(a, s, ti, qb);
         ++qb;
         if (qb * int64_t(ti) < s.n) return;
         qb = 0;
@@ -170,61 +168,56 @@ struct RowsPlace {
 
 // This CTA's stretch [begin, end) of the line, `place` at its start, and the
 // share that cuts the line.  Boundary i is at i shares, moved back to the start
-// of an item that is too short to be worth cutting; even lanes of the warp work
-// out this CTA's boundary, odd lanes the next one's.
-__device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane, int64_t &share, int64_t &begin, int64_t &end,
-                                          RowsPlace &place) {
+// of its item if that is too short to be worth cutting or the boundary lies
+// before its first tile; even lanes of the warp work out this CTA's boundary,
+// odd lanes the next one's.
+__device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane, int &share, int &begin, int &end, RowsPlace &place) {
     constexpr unsigned FULL = 0xffffffffu;
-    int64_t mine = 0, sum = 0;  // tiles of this lane's sequence (of the last batch of 32)
-    for (int i = lane; i < a.B; i += 32) sum += mine = rows_seq_tiles(a, rows_seq(a, i), ti) * a.H_kv;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    const int64_t total = sum;
-    share = rows_div(total + gridDim.x - 1, gridDim.x);
+    int mine = 0, sum = 0;  // length of this lane's sequence (of the last batch of 32)
+    for (int i = lane; i < a.B; i += 32) sum += mine = rows_seq_length(a, rows_seq(a, i), ti) * a.H_kv;
+    const int total = __reduce_add_sync(FULL, sum);
+    share = (total + int(gridDim.x) - 1) / int(gridDim.x);
     if (share < a.min_share) share = a.min_share;
-    const int64_t at = share * (blockIdx.x + (lane & 1));
-    const bool inside = at > 0 && at < total;
-    const int64_t at_a = __shfl_sync(FULL, at, 0), at_b = __shfl_sync(FULL, at, 1);
-    // the sequence that holds each
-    int64_t base = 0, seq0 = 0, per = 1;
-    int b = -1;
+    const int64_t at64 = int64_t(share) * (blockIdx.x + (lane & 1));
+    const int at = at64 < total ? int(at64) : total;
+    // the sequence that holds it
+    int base = 0, seq0 = 0, per = 1, b = -1;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        if (a.B > 32) mine = b0 + lane < a.B ? rows_seq_tiles(a, rows_seq(a, b0 + lane), ti) * a.H_kv : 0;
-        int64_t incl = mine;
+        if (a.B > 32) mine = b0 + lane < a.B ? rows_seq_length(a, rows_seq(a, b0 + lane), ti) * a.H_kv : 0;
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(FULL, incl, o);
+            const int y = __shfl_up_sync(FULL, incl, o);
             if (lane >= o) incl += y;
         }
         incl += base;
+        const int at_a = __shfl_sync(FULL, at, 0), at_b = __shfl_sync(FULL, at, 1);
         const unsigned hit_a = __ballot_sync(FULL, incl > at_a), hit_b = __ballot_sync(FULL, incl > at_b);
         const unsigned hit = lane & 1 ? hit_b : hit_a;
         const int l = hit ? __ffs(hit) - 1 : 0;
-        const int64_t tiles = __shfl_sync(FULL, mine, l), last = __shfl_sync(FULL, incl, l);
+        const int length = __shfl_sync(FULL, mine, l), last = __shfl_sync(FULL, incl, l);
         if (hit && b < 0) {
             b = b0 + l;
-            per = rows_div(tiles, a.H_kv);
-            seq0 = last - tiles;
+            per = length / a.H_kv;
+            seq0 = last - length;
         }
         base = __shfl_sync(FULL, incl, 31);
         if (hit_a && hit_b) break;
     }
     RowsPlace p;
     p.b = b;
-    p.kv = p.qb = 0;
-    p.item0 = 0;
-    int64_t bound = at <= 0 ? 0 : total;
+    p.kv = p.qb = p.item0 = 0;
+    int bound = total;
     if (b >= 0) {
         p.s = rows_seq(a, b);
-        p.kv = int(rows_div(at - seq0, per));
+        p.kv = (at - seq0) / per;
         p.item0 = seq0 + p.kv * per;
-        const int nblk = (p.s.n + ti - 1) / ti;
         // the last block that starts at or before `at`
         if (a.tree_mask) {
-            p.qb = int(rows_div(at - p.item0, rows_block_tiles(a, p.s, ti, 0)));
+            p.qb = (at - p.item0) / (a.item_cost + rows_block_tiles(a, p.s, ti, 0));
             p.item0 += rows_prefix(a, p.s, ti, p.qb);
         } else if (128 % ti == 0 || ti > 128) {
-            int lo = 0, hi = nblk - 1;
+            int lo = 0, hi = (p.s.n + ti - 1) / ti - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (p.item0 + rows_prefix(a, p.s, ti, mid) <= at) lo = mid; else hi = mid - 1;
@@ -233,12 +226,12 @@ __device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane,
             p.item0 += rows_prefix(a, p.s, ti, lo);
         } else {
             for (;; ++p.qb) {
-                const int t = rows_block_tiles(a, p.s, ti, p.qb);
+                const int t = a.item_cost + rows_block_tiles(a, p.s, ti, p.qb);
                 if (at < p.item0 + t) break;
                 p.item0 += t;
             }
         }
-        if (inside) bound = rows_block_tiles(a, p.s, ti, p.qb) <= a.split_min ? p.item0 : at;
+        bound = rows_block_tiles(a, p.s, ti, p.qb) <= a.split_min || at <= p.item0 + a.item_cost ? p.item0 : at;
     }
     begin = __shfl_sync(FULL, bound, 0);
     end = __shfl_sync(FULL, bound, 1);
@@ -249,10 +242,34 @@ __device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane,
     if (begin < end) place.s = rows_seq(a, place.b);
 }
 
-__device__ __forceinline__ void st_global_v8(float *p, const uint32_t *v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// 16 lanes x 32 columns of tensor memory, as accumulator fragments: thread i
+// receives, of column block n (8 columns), lane i / 4 columns 2 (i mod 4), + 1 in
+// r[4 n], r[4 n + 1], and lane i / 4 + 8 in r[4 n + 2], r[4 n + 3].
+__device__ __forceinline__ void rows_tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void rows_reg_fence16(uint32_t (&r)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(r[e]));
+}
+// Transposes the 4 x 4 words that the four lanes of a quad hold.
+__device__ __forceinline__ void rows_quad_transpose(uint32_t (&w)[4], int lane) {
+    const bool odd = lane & 1, up = lane & 2;
+    uint32_t x = odd ? w[0] : w[1], y = odd ? w[2] : w[3];
+    x = __shfl_xor_sync(0xffffffffu, x, 1);
+    y = __shfl_xor_sync(0xffffffffu, y, 1);
+    (odd ? w[0] : w[1]) = x;
+    (odd ? w[2] : w[3]) = y;
+    x = up ? w[0] : w[2], y = up ? w[1] : w[3];
+    x = __shfl_xor_sync(0xffffffffu, x, 2);
+    y = __shfl_xor_sync(0xffffffffu, y, 2);
+    (up ? w[0] : w[2]) = x;
+    (up ? w[1] : w[3]) = y;
 }
 
 __device__ __forceinline__ void rows_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -402,244 +419,249 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         return true;
     };
     int issued = 0, queries = 0;  // stages filled by the copy warp, items whose queries were copied
-    if (warp == C::ITEM_WARP) {
-        // ------------------------------------------------------------ items and their queries
-        int64_t share, begin, end;
-        RowsPlace w;
-        rows_plan(a, TI, lane, share, begin, end, w);
-        const int me = int(blockIdx.x);
-        RowsCut cut = {0, 0, 0, 0, 0};
-        bool ok = true;
-        int64_t at = begin;
-        for (int k = 0; ok; ++k) {
+    if (warp >= C::K_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+        if (warp == C::ITEM_WARP) {
+            // ------------------------------------------------------------ items and their queries
+            int share, begin, end;
+            RowsPlace w;
+            rows_plan(a, TI, lane, share, begin, end, w);
+            const int me = int(blockIdx.x);
+            RowsCut cut = {0, 0, 0, 0, 0};
+            bool ok = true;
+            int at = begin;
+            for (int k = 0; ok; ++k) {
+                RowsItem it;
+                it.b = -1;
+                if (at < end) {
+                    const int tiles = rows_block_tiles(a, w.s, TI, w.qb);
+                    it.b = w.b;
+                    it.kv = w.kv;
+                    it.t0 = w.qb * TI;
+                    it.ntok = min(TI, w.s.n - it.t0);
+                    it.c = w.s.c;
+                    it.n = w.s.n;
+                    it.row0 = int(w.s.row0);
+                    it.vis = a.tree_mask ? w.s.n : it.t0 + it.ntok;
+                    it.np = (w.s.c + 127) / 128;
+                    it.j0 = max(0, at - w.item0 - a.item_cost);
+                    it.j1 = min(end - w.item0 - a.item_cost, tiles);
+                    // pieces: the one that starts an item takes the CTA's second slot,
+                    // one that goes on with it the first
+                    it.slot = it.j0 == 0 && it.j1 == tiles ? -1 : 2 * me + (it.j0 == 0 ? 1 : 0);
+                    if (it.j0 == 0 && it.j1 < tiles)
+                        cut = {(w.item0 + a.item_cost + tiles - 1) / share - me + 1, it.b, it.kv, it.t0, it.ntok};
+                    at = w.item0 + a.item_cost + it.j1;
+                }
+                if (k >= 2) ok = __all_sync(FULL, dev::mbar_wait_bounded(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
+                if (!ok) break;
+                if (lane == 0) {
+                    *reinterpret_cast<RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1)) = it;
+                    dev::mbar_arrive(item_full + 8 * (k & 1));
+                }
+                if (it.b < 0) break;
+                if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
+                if (!ok) break;
+                if (lane == 0) {
+                    // one box of TB tokens x g heads per column block and query tile
+                    const int nx = it.ntok > TB ? 2 : 1;
+                    dev::mbar_arrive_expect_tx(q_full, uint32_t(nx * CB * G * TB) * 128);
+                    for (int x = 0; x < nx; ++x)
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb) {
+                            const uint32_t dst = sb + x * C::TILE_BYTES + cb * BLK;
+                            if (a.cu_seqlens)
+                                dev::tma_load_3d(dst, &a.tm_q, cb * 64, it.kv * G, it.row0 + it.t0 + x * TB, q_full);
+                            else
+                                dev::tma_load_4d(dst, &a.tm_q, cb * 64, it.kv * G, it.t0 + x * TB, it.b, q_full);
+                        }
+                }
+                queries = k + 1;
+                __syncwarp();
+                if (at < end) w.next(a, TI);
+            }
+            if (lane == 0) a.cuts[me] = cut;
+            if (me == 0)  // sequences whose arguments are out of range
+                for (int i = lane; i < a.B; i += 32)
+                    if (rows_seq(a, i).bad) dev::record_error(a.err, ERR_DEVICE_INDEX);
+            if (!ok) give_up();
+        } else if (warp == C::K_WARP) {
+            // ------------------------------------------------------------ K and V copies
+            bool ok = true;
             RowsItem it;
-            it.b = -1;
-            if (at < end) {
-                const int tiles = rows_block_tiles(a, w.s, TI, w.qb);
-                it.b = w.b;
-                it.kv = w.kv;
-                it.t0 = w.qb * TI;
-                it.ntok = min(TI, w.s.n - it.t0);
-                it.c = w.s.c;
-                it.n = w.s.n;
-                it.row0 = int(w.s.row0);
-                it.vis = a.tree_mask ? w.s.n : it.t0 + it.ntok;
-                it.np = (w.s.c + 127) / 128;
-                it.j0 = int(at - w.item0);
-                it.j1 = int(min(end - w.item0, int64_t(tiles)));
-                // pieces: the one that starts an item takes the CTA's second slot,
-                // one that goes on with it the first
-                it.slot = it.j0 == 0 && it.j1 == tiles ? -1 : 2 * me + (it.j0 == 0 ? 1 : 0);
-                if (it.j0 == 0 && it.j1 < tiles)
-                    cut = {int(rows_div(w.item0 + tiles - 1, share)) - me + 1, it.b, it.kv, it.t0, it.ntok};
-                at = w.item0 + it.j1;
-            }
-            if (k >= 2) ok = __all_sync(FULL, dev::mbar_wait_bounded(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
-            if (!ok) break;
-            if (lane == 0) {
-                *reinterpret_cast<RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1)) = it;
-                dev::mbar_arrive(item_full + 8 * (k & 1));
-            }
-            if (it.b < 0) break;
-            if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
-            if (!ok) break;
-            if (lane == 0) {
-                // one box of TB tokens x g heads per column block and query tile
-                const int nx = it.ntok > TB ? 2 : 1;
-                dev::mbar_arrive_expect_tx(q_full, uint32_t(nx * CB * G * TB) * 128);
-                for (int x = 0; x < nx; ++x)
+            for (int k = 0; ok; ++k) {
+                ok = __all_sync(FULL, take_item(k, it));
+                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+                if (it.b < 0) break;
+                const int n = it.j1 - it.j0;
+                const bool fold = it.ntok <= TB && n > 1;
+                // the tile at place i, and whether it is V
+                auto tile_at = [&](int i) { return it.j0 + (fold ? (i == 2 * n - 1 ? n - 1 : i & 1 ? (i + 1) >> 1 : i ? (i >> 1) - 1 : 0) : i >> 1); };
+                // a page's number is looked up a tile ahead
+                auto page_at = [&](int i) {
+                    if (!a.block_table || lane >= 8 || i >= 2 * n) return 0;
+                    const int j = tile_at(i), blk = 8 * j + lane;
+                    return j < it.np && blk * 16 < it.c ? __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk) : 0;
+                };
+                int next_page = page_at(0);
+                for (int i = 0; i < 2 * n; ++i) {
+                    const int page = next_page, j = tile_at(i);
+                    const bool v = fold ? i > 0 && (i == 2 * n - 1 || !(i & 1)) : i & 1;
+                    next_page = page_at(i + 1);
+                    {
+                        const int s = issued % NS;
+                        if (issued >= NS)
+                            ok = __all_sync(FULL, dev::mbar_wait_bounded(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
+                        if (!ok) break;
+                        const uint32_t dst = ring + uint32_t(s) * C::TILE_BYTES, bar = full + 8 * s;
+                        if (j >= it.np) {  // new rows
+                            const int jn = j - it.np;
+                            if (lane == 0) {
+                                dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                                const CUtensorMap *m = v ? &a.tm_v_new : &a.tm_k_new;
 #pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) {
-                        const uint32_t dst = sb + x * C::TILE_BYTES + cb * BLK;
-                        if (a.cu_seqlens)
-                            dev::tma_load_3d(dst, &a.tm_q, cb * 64, it.kv * G, it.row0 + it.t0 + x * TB, q_full);
-                        else
-                            dev::tma_load_4d(dst, &a.tm_q, cb * 64, it.kv * G, it.t0 + x * TB, it.b, q_full);
+                                for (int cb = 0; cb < CB; ++cb)
+                                    if (a.cu_seqlens)
+                                        dev::tma_load_3d(dst + cb * BLK, m, cb * 64, it.kv, it.row0 + 128 * jn, bar);
+                                    else
+                                        dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * jn, it.b * a.H_kv + it.kv, bar);
+                            }
+                        } else if (!a.block_table) {
+                            if (lane == 0) {
+                                dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                                const CUtensorMap *m = v ? &a.tm_v : &a.tm_k;
+#pragma unroll
+                                for (int cb = 0; cb < CB; ++cb)
+                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * j, a.seg_base + it.b * a.H_kv + it.kv, bar);
+                            }
+                        } else {
+                            // the pages that hold cached rows, one lane each; a page out of
+                            // range is recorded and read as zeros (behind the pool's end)
+                            const int pages = min(8, (it.c - 128 * j + 15) / 16);
+                            if (lane == 0) dev::mbar_arrive_expect_tx(bar, uint32_t(pages) * CB * 2048);
+                            __syncwarp();
+                            if (lane < pages) {
+                                const bool in = page >= 0 && page < a.num_blocks;
+                                if (!in) dev::record_error(a.err, ERR_DEVICE_INDEX);
+                                dev::tma_load_5d(dst + lane * (CB * 2048), v ? &a.tm_v : &a.tm_k, 0, 0, 0, it.kv,
+                                                 in ? a.seg_base + page : a.pool_end, bar);
+                            }
+                        }
+                        ++issued;
                     }
-            }
-            queries = k + 1;
-            __syncwarp();
-            if (at < end) w.next(a, TI);
-        }
-        if (lane == 0) a.cuts[me] = cut;
-        if (me == 0)  // sequences whose arguments are out of range
-            for (int i = lane; i < a.B; i += 32)
-                if (rows_seq(a, i).bad) dev::record_error(a.err, ERR_DEVICE_INDEX);
-        if (!ok) give_up();
-    } else if (warp == C::K_WARP) {
-        // ------------------------------------------------------------ K and V copies
-        bool ok = true;
-        RowsItem it;
-        for (int k = 0; ok; ++k) {
-            ok = __all_sync(FULL, take_item(k, it));
-            __syncwarp();
-            if (!ok) break;
-            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
-            if (it.b < 0) break;
-            const int n = it.j1 - it.j0;
-            const bool fold = it.ntok <= TB && n > 1;
-            // the tile at place i, and whether it is V
-            auto tile_at = [&](int i) { return it.j0 + (fold ? (i == 2 * n - 1 ? n - 1 : i & 1 ? (i + 1) >> 1 : i ? (i >> 1) - 1 : 0) : i >> 1); };
-            // a page's number is looked up a tile ahead
-            auto page_at = [&](int i) {
-                if (!a.block_table || lane >= 8 || i >= 2 * n) return 0;
-                const int j = tile_at(i), blk = 8 * j + lane;
-                return j < it.np && blk * 16 < it.c ? __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk) : 0;
-            };
-            int next_page = page_at(0);
-            for (int i = 0; i < 2 * n; ++i) {
-                const int page = next_page, j = tile_at(i);
-                const bool v = fold ? i > 0 && (i == 2 * n - 1 || !(i & 1)) : i & 1;
-                next_page = page_at(i + 1);
-                {
-                    const int s = issued % NS;
-                    if (issued >= NS)
-                        ok = __all_sync(FULL, dev::mbar_wait_bounded(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
-                    if (!ok) break;
-                    const uint32_t dst = ring + uint32_t(s) * C::TILE_BYTES, bar = full + 8 * s;
-                    if (j >= it.np) {  // new rows
-                        const int jn = j - it.np;
-                        if (lane == 0) {
-                            dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-                            const CUtensorMap *m = v ? &a.tm_v_new : &a.tm_k_new;
-#pragma unroll
-                            for (int cb = 0; cb < CB; ++cb)
-                                if (a.cu_seqlens)
-                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, it.kv, it.row0 + 128 * jn, bar);
-                                else
-                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * jn, it.b * a.H_kv + it.kv, bar);
-                        }
-                    } else if (!a.block_table) {
-                        if (lane == 0) {
-                            dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-                            const CUtensorMap *m = v ? &a.tm_v : &a.tm_k;
-#pragma unroll
-                            for (int cb = 0; cb < CB; ++cb)
-                                dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * j, a.seg_base + it.b * a.H_kv + it.kv, bar);
-                        }
-                    } else {
-                        // the pages that hold cached rows, one lane each; a page out of
-                        // range is recorded and read as zeros (behind the pool's end)
-                        const int pages = min(8, (it.c - 128 * j + 15) / 16);
-                        if (lane == 0) dev::mbar_arrive_expect_tx(bar, uint32_t(pages) * CB * 2048);
-                        __syncwarp();
-                        if (lane < pages) {
-                            const bool in = page >= 0 && page < a.num_blocks;
-                            if (!in) dev::record_error(a.err, ERR_DEVICE_INDEX);
-                            dev::tma_load_5d(dst + lane * (CB * 2048), v ? &a.tm_v : &a.tm_k, 0, 0, 0, it.kv,
-                                             in ? a.seg_base + page : a.pool_end, bar);
-                        }
-                    }
-                    ++issued;
                 }
             }
-        }
-        if (!ok) give_up();
-    } else if (warp == C::MMA_WARP) {
-        // ------------------------------------------------------------ MMAs
-        // The whole warp walks the loop, one elected lane issues: the operands'
-        // descriptors then stay warp-uniform, and each is its tile's plus a constant.
-        const bool leader = rows_elect();
-        constexpr uint32_t HI1 = rows_desc_hi(1024), HI4 = rows_desc_hi(4096);
-        bool ok = true;
-        RowsItem it;
-        uint32_t st = 0;                                // places consumed so far
-        uint32_t tiles[2] = {0, 0}, items[2] = {0, 0};  // of each stream
-        auto stage_wait = [&](uint32_t i) { return dev::mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, flags, a.timeout_ns); };
-        auto issue_s = [&](int x, int qx, uint32_t i, bool paged) {
-            const uint32_t kt = (ring + (i % NS) * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
-            if (leader) {
-                if (CB == 2 && paged) {
+            if (!ok) give_up();
+        } else if (warp == C::MMA_WARP) {
+            // ------------------------------------------------------------ MMAs
+            // The whole warp walks the loop, one elected lane issues: the operands'
+            // descriptors then stay warp-uniform, and each is its tile's plus a constant.
+            const bool leader = rows_elect();
+            constexpr uint32_t HI1 = rows_desc_hi(1024), HI4 = rows_desc_hi(4096);
+            bool ok = true;
+            RowsItem it;
+            uint32_t st = 0;                                // places consumed so far
+            uint32_t tiles_a = 0, tiles_b = 0, items_a = 0, items_b = 0;  // of each stream
+            auto stage_wait = [&](uint32_t i) { return dev::mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, flags, a.timeout_ns); };
+            auto issue_s = [&](int x, int qx, uint32_t i, bool paged) {
+                const uint32_t kt = (ring + (i % NS) * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
+                if (leader) {
+                    if (CB == 2 && paged) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                tc::mma_f16_ss(s_t + 64 * h, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
+                                               rows_desc(kt + (((ks >> 2) * 2048 + (ks & 3) * 32 + h * 1024) >> 4), HI4), IDESC_S64, ks > 0);
+                    } else {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
-                            tc::mma_f16_ss(s_t + 64 * h, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
-                                           rows_desc(kt + (((ks >> 2) * 2048 + (ks & 3) * 32 + h * 1024) >> 4), HI4), IDESC_S64, ks > 0);
-                } else {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        tc::mma_f16_ss(s_t, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
-                                       rows_desc(kt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1), IDESC_S, ks > 0);
+                            tc::mma_f16_ss(s_t, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
+                                           rows_desc(kt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1), IDESC_S, ks > 0);
+                    }
+                    tc::commit(s_full + 8 * x);
                 }
-                tc::commit(s_full + 8 * x);
-            }
-        };
-        auto issue_pv = [&](int x, uint32_t i, bool paged, bool first) {
-            const uint32_t vt = (ring + (i % NS) * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
-            if (leader) {
-                if (CB == 2 && paged) {
+            };
+            auto issue_pv = [&](int x, uint32_t i, bool paged, bool first) {
+                const uint32_t vt = (ring + (i % NS) * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
+                if (leader) {
+                    if (CB == 2 && paged) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + (((ks & 3) * 8192 + (ks >> 2) * 1024) >> 4) + ((2048 >> 4) << 16), HI4),
-                                       IDESC_O, ks > 0 || !first);
-                } else {
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + (((ks & 3) * 8192 + (ks >> 2) * 1024) >> 4) + ((2048 >> 4) << 16), HI4),
+                                           IDESC_O, ks > 0 || !first);
+                    } else {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 2048) >> 4) + ((BLK >> 4) << 16), HI1), IDESC_O, ks > 0 || !first);
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 2048) >> 4) + ((BLK >> 4) << 16), HI1), IDESC_O, ks > 0 || !first);
+                    }
                 }
-            }
-        };
-        auto commit_to = [&](uint32_t bar) {
-            if (leader) tc::commit(bar);
-        };
-        for (int k = 0; ok; ++k) {
-            ok = __all_sync(FULL, take_item(k, it));
-            __syncwarp();
-            if (!ok) break;
-            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
-            if (it.b < 0) break;
-            const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
-            const bool fold = nx == 1 && n > 1;
-            auto is_paged = [&](int j) { return a.block_table && it.j0 + j < it.np; };
-            ok = dev::mbar_wait_bounded(q_full, uint32_t(k) & 1, flags, a.timeout_ns) && stage_wait(st);
-            if (fold) ok = ok && stage_wait(st + 1);
-            ok = __all_sync(FULL, ok);
-            if (!ok) break;
-            tc::fence_after();
-            issue_s(0, 0, st, is_paged(0));
-            if (fold) commit_to(empty + 8 * (st % NS));
-            if (fold || nx == 2) issue_s(1, fold ? 0 : 1, fold ? st + 1 : st, is_paged(fold ? 1 : 0));
-            commit_to(empty + 8 * ((fold ? st + 1 : st) % NS));
-            if (n == (fold ? 2 : 1)) commit_to(q_empty);
-            const int steps = fold ? n : n * nx;
-            for (int u = 0; u < steps; ++u) {
-                const int x = fold || nx == 2 ? u & 1 : 0, j = fold || nx == 1 ? u : u >> 1;
-                const int jn = fold ? j + 2 : j + 1;
-                const bool first = fold ? j < 2 : j == 0, release = fold || x == nx - 1;
-                const uint32_t sv = st + rows_v_place(fold, j, n);
-                ok = dev::mbar_wait_bounded(p_full + 8 * x, tiles[x] & 1, flags, a.timeout_ns) && stage_wait(sv);
-                if (ok && first && items[x] > 0) ok = dev::mbar_wait_bounded(o_free + 8 * x, (items[x] - 1) & 1, flags, a.timeout_ns);
+            };
+            auto commit_to = [&](uint32_t bar) {
+                if (leader) tc::commit(bar);
+            };
+            for (int k = 0; ok; ++k) {
+                ok = __all_sync(FULL, take_item(k, it));
+                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+                if (it.b < 0) break;
+                const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
+                const bool fold = nx == 1 && n > 1;
+                auto is_paged = [&](int j) { return a.block_table && it.j0 + j < it.np; };
+                ok = dev::mbar_wait_bounded(q_full, uint32_t(k) & 1, flags, a.timeout_ns) && stage_wait(st);
+                if (fold) ok = ok && stage_wait(st + 1);
                 ok = __all_sync(FULL, ok);
                 if (!ok) break;
-                ++tiles[x];
                 tc::fence_after();
-                issue_pv(x, sv, is_paged(j), first);
-                if (release) commit_to(empty + 8 * (sv % NS));
-                if (jn < n) {
-                    const uint32_t sk = st + rows_k_place(fold, jn);
-                    ok = __all_sync(FULL, stage_wait(sk));
+                issue_s(0, 0, st, is_paged(0));
+                if (fold) commit_to(empty + 8 * (st % NS));
+                if (fold || nx == 2) issue_s(1, fold ? 0 : 1, fold ? st + 1 : st, is_paged(fold ? 1 : 0));
+                commit_to(empty + 8 * ((fold ? st + 1 : st) % NS));
+                if (n == (fold ? 2 : 1)) commit_to(q_empty);
+                const int steps = fold ? n : n * nx;
+                for (int u = 0; u < steps; ++u) {
+                    const int x = fold || nx == 2 ? u & 1 : 0, j = fold || nx == 1 ? u : u >> 1;
+                    const int jn = fold ? j + 2 : j + 1;
+                    const bool first = fold ? j < 2 : j == 0, release = fold || x == nx - 1;
+                    const uint32_t sv = st + rows_v_place(fold, j, n);
+                    ok = dev::mbar_wait_bounded(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1, flags, a.timeout_ns) && stage_wait(sv);
+                    const uint32_t items = x ? items_b : items_a;
+                    if (ok && first && items > 0) ok = dev::mbar_wait_bounded(o_free + 8 * x, (items - 1) & 1, flags, a.timeout_ns);
+                    ok = __all_sync(FULL, ok);
                     if (!ok) break;
+                    ++(x ? tiles_b : tiles_a);
                     tc::fence_after();
-                    issue_s(x, fold ? 0 : x, sk, is_paged(jn));
-                    if (release) {
-                        commit_to(empty + 8 * (sk % NS));
-                        if (jn == n - 1) commit_to(q_empty);
+                    issue_pv(x, sv, is_paged(j), first);
+                    if (release) commit_to(empty + 8 * (sv % NS));
+                    if (jn < n) {
+                        const uint32_t sk = st + rows_k_place(fold, jn);
+                        ok = __all_sync(FULL, stage_wait(sk));
+                        if (!ok) break;
+                        tc::fence_after();
+                        issue_s(x, fold ? 0 : x, sk, is_paged(jn));
+                        if (release) {
+                            commit_to(empty + 8 * (sk % NS));
+                            if (jn == n - 1) commit_to(q_empty);
+                        }
+                    } else {
+                        commit_to(o_full + 8 * x);
+                        ++(x ? items_b : items_a);
                     }
-                } else {
-                    commit_to(o_full + 8 * x);
-                    ++items[x];
                 }
+                st += 2 * n;
             }
-            st += 2 * n;
+            if (!ok) give_up();
+            commit_to(mma_done);  // every MMA is done before tensor memory is freed
+            const volatile int never = 0;
+            dev::mbar_wait_bounded(mma_done, 0, &never, a.timeout_ns);
+            __syncwarp();
         }
-        if (!ok) give_up();
-        commit_to(mma_done);  // every MMA is done before tensor memory is freed
-        const volatile int never = 0;
-        dev::mbar_wait_bounded(mma_done, 0, &never, a.timeout_ns);
-        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
         const int x = warp >> 2, qd = warp & 3;
         const int r = 32 * qd + lane;           // query row = TMEM lane
         const int tt = r / G, head = r - tt * G;
@@ -649,21 +671,25 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
         bool ok = true;
         uint32_t st = 0, gt = 0, gi = 0, folds = 0;  // ring position; tiles, items and folded items of this stream so far
-        RowsItem it;
         for (int k = 0; ok; ++k) {
-            ok = __all_sync(FULL, take_item(k, it));
-            __syncwarp();
+            // (the item is read where it is, which spares registers, and let go at its end)
+            ok = __all_sync(FULL, dev::mbar_wait_bounded(item_full + 8 * (k & 1), uint32_t(k >> 1) & 1, flags, a.timeout_ns));
             if (!ok) break;
-            if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+            const RowsItem &it = *reinterpret_cast<const RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1));
             if (it.b < 0) break;
+            auto leave = [&]() {
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
+            };
             const int n = it.j1 - it.j0;
             const bool two = it.ntok > TB, fold = !two && n > 1;
             if (x == 1 && !two && !fold) {  // nothing for stream B
                 st += 2 * n;
+                leave();
                 continue;
             }
             const int qx = two ? x : 0;  // query tile of this stream
-            // (the slot of item k - 3, which every role has left: it has taken item k - 2)
+            // (the slot of item k - 3, which every role has left: item k is there)
             if (threadIdx.x == 0) odd[(k + 1) & 3] = 0;
             const int t = it.t0 + qx * TB + tt;              // token
             const bool row_ok = tt < TB && qx * TB + tt < it.ntok;
@@ -758,8 +784,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         uint32_t o[16];
                         rows_tmem_ld16(o_t + 16 * q, o);
                         tc::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(o[e]));
+                        rows_reg_fence16(o);
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), c2);
@@ -802,6 +827,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(fold_bar);
                 ++gi;
+                leave();
                 continue;
             }
             ok = dev::mbar_wait_bounded(o_full + 8 * x, gi & 1, flags, a.timeout_ns);
@@ -826,16 +852,72 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             const float inv = l > 0.f ? 1.f / l : 0.f;
             RowsSeq sq;
             sq.row0 = it.row0;
-            uint4 *orow = nullptr;
-            float *prow = nullptr;
-            if (row_ok) {
-                if (it.slot < 0) {
-                    orow = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + head, t, D));
-                } else {
-                    const int64_t row = int64_t(it.slot) * 256 + 128 * qx + r;
-                    prow = a.part_acc + row * D;
-                    *reinterpret_cast<float2 *>(a.part_ml + 2 * row) = make_float2(m_run, l);
+            auto release = [&]() {  // the accumulators are read: the next item's PV may overwrite them
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    dev::mbar_arrive(o_free + 8 * x);
+                    if (fold) dev::mbar_arrive(o_free);
                 }
+            };
+            if (it.slot < 0 && !any_odd) {
+                // the whole item: fragments of 16 query rows x 32 columns at a time,
+                // so that four lanes hold 32 columns of a row and, transposed,
+                // write 64 contiguous bytes (a row per lane, 16 bytes at a time,
+                // keeps the store path busy four times as long, and with it
+                // every barrier of the CTA)
+                const int quad = lane >> 2, ql = lane & 3;
+                T *rows_out[4];  // query rows 8 i + quad of the warp's 32
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 32 * qd + 8 * i + quad, rt = rr / G, tok = qx * TB + rt;
+                    rows_out[i] = rt < TB && tok < it.ntok
+                                      ? reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + (rr - rt * G), it.t0 + tok, D) + 8 * ql
+                                      : nullptr;
+                }
+                // a row of zeros where nothing was seen (whatever the accumulator holds)
+                const float g_b = l > 0.f ? f_b * inv : 0.f, g_a = l > 0.f ? f_a * inv : 0.f;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t o[16], oa[16];
+                        const uint32_t at = o_t + (uint32_t(16 * h) << 16) + 32 * q;
+                        rows_tmem_ld_frag(at, o);
+                        if (fold) rows_tmem_ld_frag(at - D, oa);
+                        tc::tmem_ld_wait();
+                        rows_reg_fence16(o);
+                        if (fold) rows_reg_fence16(oa);
+                        if (q == D / 32 - 1 && h == 1) release();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int src = 16 * h + 8 * i + quad;
+                            const float gb = __shfl_sync(FULL, g_b, src), ga = __shfl_sync(FULL, g_a, src);
+                            uint32_t w[4];
+#pragma unroll
+                            for (int n4 = 0; n4 < 4; ++n4) {
+                                float y0 = __uint_as_float(o[4 * n4 + 2 * i]) * gb, y1 = __uint_as_float(o[4 * n4 + 2 * i + 1]) * gb;
+                                if (fold) {
+                                    y0 = fmaf(__uint_as_float(oa[4 * n4 + 2 * i]), ga, y0);
+                                    y1 = fmaf(__uint_as_float(oa[4 * n4 + 2 * i + 1]), ga, y1);
+                                }
+                                w[n4] = Ops::pack(y0, y1);
+                            }
+                            rows_quad_transpose(w, lane);
+                            T *to = rows_out[2 * h + i];
+                            if (to) *reinterpret_cast<uint4 *>(to + 32 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                leave();
+                continue;
+            }
+            // a piece: its accumulator, four columns of the tile's rows after one
+            // another; or an item with infinities or NaN among its V rows
+            float *prow = nullptr;
+            if (row_ok && it.slot >= 0) {
+                prow = a.part_acc + int64_t(it.slot) * 256 * D + 4 * (128 * qx + r);
+                reinterpret_cast<float2 *>(a.part_ml)[int64_t(it.slot) * 256 + 128 * qx + r] = make_float2(m_run, l);
             }
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -854,22 +936,14 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     tc::tmem_ld_wait();
                     tc::reg_fence(o);
                 }
-                if (q == D / 32 - 1) {  // the accumulators are read: the next item's PV may overwrite them
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        dev::mbar_arrive(o_free + 8 * x);
-                        if (fold) dev::mbar_arrive(o_free);
-                    }
-                }
+                if (q == D / 32 - 1) release();
                 if (any_odd && row_ok) {
-                    // infinities and NaN among the V rows that this row sees (of
-                    // the tiles that were searched: those some row does not see whole)
+                    // add them back where the row sees them (of the tiles that were
+                    // searched: those some row does not see whole)
                     for (int jt = max(it.j0, it.np); jt < it.j1; ++jt) {
                         const int key0 = 128 * (jt - it.np), nv = min(128, it.vis - key0);
                         if (!(nv < 128 || a.tree_mask || key0 + 127 > it.t0)) continue;
-                        for (int s = 0; s < nv; ++s) {
-                            const int key = key0 + s;
+                        for (int key = key0; key < key0 + nv; ++key) {
                             const bool see = a.tree_mask ? __ldg(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + (key >> 5)) >> (key & 31) & 1u
                                                          : key <= t;
                             if (!see) continue;
@@ -882,20 +956,23 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         }
                     }
                 }
-                if (orow) {
+                if (prow) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(prow + int64_t(8 * q + e / 4) * 1024) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (row_ok) {
+                    T *orow = reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + head, t, D) + 32 * q;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t u[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             u[i] = l > 0.f ? Ops::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv) : 0u;
-                        orow[4 * q + e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4 *>(orow + e) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                } else if (prow) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) st_global_v8(prow + 32 * q + e, o + e);
                 }
             }
+            leave();
         }
         if (!ok) give_up();
     }
@@ -919,65 +996,48 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     }
 }
 
-// Folds the pieces of the items that CTA boundaries cut.  Block (i, y): rows
-// [8 y, 8 y + 8) of the item that CTA i started; a warp takes one row, with the
-// lanes on its columns:  out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M).
+// Folds the pieces of the items that CTA boundaries cut.  Block (i, y): 32 query
+// rows x 64 columns of the item that CTA i started; a thread takes eight columns
+// of a row, consecutive threads consecutive rows, as the pieces are laid out:
+// out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsTcArgs a) {
-    constexpr int EPL = D / 32;
     dev::grid_dependency_wait();
     dev::allow_dependents();
-    const int i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int i = blockIdx.x;
     const RowsCut cut = a.cuts[i];
     if (cut.pieces == 0) return;
     const int G = a.group, TB = 128 / G;
-    const int nt = blockIdx.y * 8 + warp;   // row of the item: (token, head)
-    if (nt >= cut.ntok * G) return;
-    const int tok = nt / G, head = nt - tok * G, x = tok / TB;
-    const int r = 128 * x + (tok - x * TB) * G + head;
-    auto row_of = [&](int p) { return int64_t(p == 0 ? 2 * i + 1 : 2 * (i + p)) * 256 + r; };
-    float M = -INFINITY;
-    for (int p = lane; p < cut.pieces; p += 32) M = fmaxf(M, __ldcg(a.part_ml + 2 * row_of(p)));
+    const int yr = blockIdx.y / (D / 64), yc = blockIdx.y % (D / 64);
+    const int r = 32 * yr + (threadIdx.x & 31), col = 64 * yc + 8 * (threadIdx.x >> 5);
+    const int x = r >> 7, rt = (r & 127) / G, head = (r & 127) - rt * G, tok = x * TB + rt;
+    if (rt >= TB || tok >= cut.ntok) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + r;
+    const float *acc = a.part_acc + 4 * r + (col / 4) * 1024;
+    auto slot = [&](int p) { return int64_t(p == 0 ? 2 * i + 1 : 2 * (i + p)) * 256; };
+    float M = -INFINITY, L = 0.f, o[8];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, acc[EPL];
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-    if (M > -INFINITY) {
-        for (int p0 = 0; p0 < cut.pieces; p0 += 32) {
-            const int p = p0 + lane;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (p < cut.pieces) ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + 2 * row_of(p)));
-            const float e_lane = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-            float ll = ml.y * e_lane;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
-            L += ll;
-            const int np = min(32, cut.pieces - p0);
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll 4
-            for (int q = 0; q < np; ++q) {
-                const float f = __shfl_sync(0xffffffffu, e_lane, q);
-                const float *src = a.part_acc + row_of(p0 + q) * D + lane * EPL;
-                if constexpr (EPL == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                    acc[0] = fmaf(v.x, f, acc[0]), acc[1] = fmaf(v.y, f, acc[1]), acc[2] = fmaf(v.z, f, acc[2]), acc[3] = fmaf(v.w, f, acc[3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                    acc[0] = fmaf(v.x, f, acc[0]), acc[1] = fmaf(v.y, f, acc[1]);
-                }
-            }
-        }
+    for (int p = 0; p < cut.pieces; ++p) {
+        const float2 y = __ldcg(ml + slot(p));
+        const float4 u = __ldcg(reinterpret_cast<const float4 *>(acc + slot(p) * D));
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(acc + slot(p) * D + 1024));
+        if (y.x == -INFINITY) continue;  // the row sees nothing of this piece
+        const float m = fmaxf(M, y.x), fo = M == -INFINITY ? 0.f : ex2_approx(M - m), f = ex2_approx(y.x - m);
+        M = m;
+        L = L * fo + y.y * f;
+        const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(w[e], f, o[e] * fo);
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     const RowsSeq s = rows_seq(a, cut.b);
-    T *o = reinterpret_cast<T *>(a.out) + rows_offset(a, s, cut.b, a.H_kv * G, cut.kv * G + head, cut.t0 + tok, D) + lane * EPL;
-    uint32_t u[EPL / 2];
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < EPL; e += 2) u[e / 2] = M > -INFINITY ? MmaOps<T>::pack(acc[e] * inv, acc[e + 1] * inv) : 0u;
-    if constexpr (EPL == 4)
-        *reinterpret_cast<uint2 *>(o) = make_uint2(u[0], u[1]);
-    else
-        *reinterpret_cast<uint32_t *>(o) = u[0];
+    for (int e = 0; e < 4; ++e) w[e] = MmaOps<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+    T *to = reinterpret_cast<T *>(a.out) + rows_offset(a, s, cut.b, a.H_kv * G, cut.kv * G + head, cut.t0 + tok, D) + col;
+    *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T, int D>
@@ -985,12 +1045,13 @@ cudaError_t set_rows_tc_max_smem() {
     return cudaFuncSetAttribute(rows_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsTcCfg<D>::SMEM);
 }
 
-// combine_rows: query rows of the largest item; 0 where no item can be cut.
+// combine_rows: rows of the two query tiles that an item can use; 0 where no
+// item can be cut.
 template <typename T, int D>
 cudaError_t launch_rows_tc(const RowsTcArgs &a, int grid, int combine_rows, cudaStream_t s) {
     const cudaError_t e = launch_pdl(rows_tc_kernel<T, D>, dim3(grid), dim3(RowsTcCfg<D>::THREADS), RowsTcCfg<D>::SMEM, s, a);
     if (e != cudaSuccess || combine_rows == 0 || grid == 1) return e;
-    return launch_pdl(rows_combine_kernel<T, D>, dim3(grid, (combine_rows + 7) / 8), dim3(256), 0, s, a);
+    return launch_pdl(rows_combine_kernel<T, D>, dim3(grid, (combine_rows + 31) / 32 * (D / 64)), dim3(256), 0, s, a);
 }
 
 template <typename T, int D>
