@@ -103,6 +103,22 @@ struct RowsTcCfg {
     }
 };
 
+// dev::mbar_wait_bounded, but 64 tries pass before the abort flag and the timer
+// are looked at: reading them between tries cost each hand-over between the
+// softmax and the MMAs about 400 cycles, a tenth of a key tile's time.
+__device__ __forceinline__ bool rows_wait(uint32_t bar, uint32_t parity, const volatile int *abort, unsigned long long timeout_ns) {
+    if (dev::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = dev::global_timer_ns();
+    for (uint32_t it = 0; it < (1u << 24); ++it) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (dev::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (dev::global_timer_ns() - t0 > timeout_ns) return false;
+    }
+    return false;
+}
+
 // A piece of work as the roles see it: tokens [t0, t0 + ntok) of (b, kv) against
 // key tiles [j0, j1).  b < 0: no more work.
 struct RowsItem {
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     };
     // the k-th item (k = 0, 1, ...) out of its slot; false on a timeout
     auto take_item = [&](int k, RowsItem &it) {
-        const bool w = dev::mbar_wait_bounded(item_full + 8 * (k & 1), uint32_t(k >> 1) & 1, flags, a.timeout_ns);
+        const bool w = rows_wait(item_full + 8 * (k & 1), uint32_t(k >> 1) & 1, flags, a.timeout_ns);
         if (!w) return false;
         it = *reinterpret_cast<const RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1));
         return true;
@@ -453,14 +469,14 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         cut = {(w.item0 + a.item_cost + tiles - 1) / share - me + 1, it.b, it.kv, it.t0, it.ntok};
                     at = w.item0 + a.item_cost + it.j1;
                 }
-                if (k >= 2) ok = __all_sync(FULL, dev::mbar_wait_bounded(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
+                if (k >= 2) ok = __all_sync(FULL, rows_wait(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
                 if (!ok) break;
                 if (lane == 0) {
                     *reinterpret_cast<RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1)) = it;
                     dev::mbar_arrive(item_full + 8 * (k & 1));
                 }
                 if (it.b < 0) break;
-                if (k >= 1) ok = __all_sync(FULL, dev::mbar_wait_bounded(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
+                if (k >= 1) ok = __all_sync(FULL, rows_wait(q_empty, uint32_t(k - 1) & 1, flags, a.timeout_ns));
                 if (!ok) break;
                 if (lane == 0) {
                     // one box of TB tokens x g heads per column block and query tile
@@ -513,7 +529,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     {
                         const int s = issued % NS;
                         if (issued >= NS)
-                            ok = __all_sync(FULL, dev::mbar_wait_bounded(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
+                            ok = __all_sync(FULL, rows_wait(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
                         if (!ok) break;
                         const uint32_t dst = ring + uint32_t(s) * C::TILE_BYTES, bar = full + 8 * s;
                         if (j >= it.np) {  // new rows
@@ -558,15 +574,22 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             // ------------------------------------------------------------ MMAs
             // The whole warp walks the loop, one elected lane issues: the operands'
             // descriptors then stay warp-uniform, and each is its tile's plus a constant.
+            // Tiles are taken in ring order, ahead of the wait for P: what stands
+            // between that wait and the MMAs is idle time of the tensor cores.
             const bool leader = rows_elect();
             constexpr uint32_t HI1 = rows_desc_hi(1024), HI4 = rows_desc_hi(4096);
             bool ok = true;
             RowsItem it;
-            uint32_t st = 0;                                // places consumed so far
-            uint32_t tiles_a = 0, tiles_b = 0, items_a = 0, items_b = 0;  // of each stream
-            auto stage_wait = [&](uint32_t i) { return dev::mbar_wait_bounded(full + 8 * (i % NS), (i / NS) & 1, flags, a.timeout_ns); };
-            auto issue_s = [&](int x, int qx, uint32_t i, bool paged) {
-                const uint32_t kt = (ring + (i % NS) * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
+            uint32_t stage = 0, phase = 0;                                   // next tile of the ring
+            uint32_t tiles_a = 0, tiles_b = 0, items_a = 0, items_b = 0;     // of each stream
+            auto take_tile = [&]() {
+                ok = ok && rows_wait(full + 8 * stage, phase, flags, a.timeout_ns);
+                const uint32_t s = stage;
+                if (++stage == NS) stage = 0, phase ^= 1;
+                return s;
+            };
+            auto issue_s = [&](int x, int qx, uint32_t s, bool paged) {
+                const uint32_t kt = (ring + s * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
                 if (leader) {
                     if (CB == 2 && paged) {
 #pragma unroll
@@ -584,8 +607,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     tc::commit(s_full + 8 * x);
                 }
             };
-            auto issue_pv = [&](int x, uint32_t i, bool paged, bool first) {
-                const uint32_t vt = (ring + (i % NS) * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
+            auto issue_pv = [&](int x, uint32_t s, bool paged, bool first) {
+                const uint32_t vt = (ring + s * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
                 if (leader) {
                     if (CB == 2 && paged) {
 #pragma unroll
@@ -610,53 +633,58 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 if (it.b < 0) break;
                 const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
                 const bool fold = nx == 1 && n > 1;
-                auto is_paged = [&](int j) { return a.block_table && it.j0 + j < it.np; };
-                ok = dev::mbar_wait_bounded(q_full, uint32_t(k) & 1, flags, a.timeout_ns) && stage_wait(st);
-                if (fold) ok = ok && stage_wait(st + 1);
-                ok = __all_sync(FULL, ok);
+                const int cached = a.block_table ? it.np - it.j0 : 0;  // the item's tiles j < cached are pages
+                ok = rows_wait(q_full, uint32_t(k) & 1, flags, a.timeout_ns);
+                uint32_t sk = take_tile(), sv = 0;
                 if (!ok) break;
                 tc::fence_after();
-                issue_s(0, 0, st, is_paged(0));
-                if (fold) commit_to(empty + 8 * (st % NS));
-                if (fold || nx == 2) issue_s(1, fold ? 0 : 1, fold ? st + 1 : st, is_paged(fold ? 1 : 0));
-                commit_to(empty + 8 * ((fold ? st + 1 : st) % NS));
+                issue_s(0, 0, sk, 0 < cached);
+                if (fold) {
+                    commit_to(empty + 8 * sk);
+                    sk = take_tile();
+                    if (!ok) break;
+                    tc::fence_after();
+                    issue_s(1, 0, sk, 1 < cached);
+                } else if (nx == 2) {
+                    issue_s(1, 1, sk, 0 < cached);
+                }
+                commit_to(empty + 8 * sk);
                 if (n == (fold ? 2 : 1)) commit_to(q_empty);
                 const int steps = fold ? n : n * nx;
                 for (int u = 0; u < steps; ++u) {
                     const int x = fold || nx == 2 ? u & 1 : 0, j = fold || nx == 1 ? u : u >> 1;
-                    const int jn = fold ? j + 2 : j + 1;
-                    const bool first = fold ? j < 2 : j == 0, release = fold || x == nx - 1;
-                    const uint32_t sv = st + rows_v_place(fold, j, n);
-                    ok = dev::mbar_wait_bounded(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1, flags, a.timeout_ns) && stage_wait(sv);
+                    const int jn = fold ? j + 2 : j + 1;  // the stream's next tile
+                    const bool first = fold ? j < 2 : j == 0, take = fold || x == 0, release = fold || x == nx - 1;
+                    if (take) {
+                        sv = take_tile();
+                        if (jn < n) sk = take_tile();
+                    }
                     const uint32_t items = x ? items_b : items_a;
-                    if (ok && first && items > 0) ok = dev::mbar_wait_bounded(o_free + 8 * x, (items - 1) & 1, flags, a.timeout_ns);
-                    ok = __all_sync(FULL, ok);
+                    if (first && items > 0) ok = ok && rows_wait(o_free + 8 * x, (items - 1) & 1, flags, a.timeout_ns);
+                    ok = ok && rows_wait(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1, flags, a.timeout_ns);
                     if (!ok) break;
                     ++(x ? tiles_b : tiles_a);
                     tc::fence_after();
-                    issue_pv(x, sv, is_paged(j), first);
-                    if (release) commit_to(empty + 8 * (sv % NS));
+                    issue_pv(x, sv, j < cached, first);
                     if (jn < n) {
-                        const uint32_t sk = st + rows_k_place(fold, jn);
-                        ok = __all_sync(FULL, stage_wait(sk));
-                        if (!ok) break;
-                        tc::fence_after();
-                        issue_s(x, fold ? 0 : x, sk, is_paged(jn));
+                        if (release) commit_to(empty + 8 * sv);
+                        issue_s(x, fold ? 0 : x, sk, jn < cached);
                         if (release) {
-                            commit_to(empty + 8 * (sk % NS));
+                            commit_to(empty + 8 * sk);
                             if (jn == n - 1) commit_to(q_empty);
                         }
                     } else {
                         commit_to(o_full + 8 * x);
+                        if (release) commit_to(empty + 8 * sv);
                         ++(x ? items_b : items_a);
                     }
                 }
-                st += 2 * n;
             }
+            ok = __all_sync(FULL, ok);
             if (!ok) give_up();
             commit_to(mma_done);  // every MMA is done before tensor memory is freed
             const volatile int never = 0;
-            dev::mbar_wait_bounded(mma_done, 0, &never, a.timeout_ns);
+            rows_wait(mma_done, 0, &never, a.timeout_ns);
             __syncwarp();
         }
     } else {
@@ -665,6 +693,13 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         const int x = warp >> 2, qd = warp & 3;
         const int r = 32 * qd + lane;           // query row = TMEM lane
         const int tt = r / G, head = r - tt * G;
+        int frag_tok[4], frag_head[4];  // token and head of query row 8 i + lane / 4 of the warp's 32
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rr = 32 * qd + 8 * i + (lane >> 2);
+            frag_tok[i] = rr / G;
+            frag_head[i] = rr - frag_tok[i] * G;
+        }
         const int H = a.H_kv * G;
         const uint32_t lane_base = uint32_t(qd * 32) << 16;
         const uint32_t s_t = tmem + lane_base + C::S_COL + 128 * x, o_t = tmem + lane_base + C::O_COL + D * x;
@@ -673,7 +708,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         uint32_t st = 0, gt = 0, gi = 0, folds = 0;  // ring position; tiles, items and folded items of this stream so far
         for (int k = 0; ok; ++k) {
             // (the item is read where it is, which spares registers, and let go at its end)
-            ok = __all_sync(FULL, dev::mbar_wait_bounded(item_full + 8 * (k & 1), uint32_t(k >> 1) & 1, flags, a.timeout_ns));
+            ok = __all_sync(FULL, rows_wait(item_full + 8 * (k & 1), uint32_t(k >> 1) & 1, flags, a.timeout_ns));
             if (!ok) break;
             const RowsItem &it = *reinterpret_cast<const RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1));
             if (it.b < 0) break;
@@ -698,7 +733,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             float2 l2 = make_float2(0.f, 0.f);
             const int j_first = fold ? x : 0;
             for (int j = j_first; j < n; j += fold ? 2 : 1, ++gt) {
-                ok = __all_sync(FULL, dev::mbar_wait_bounded(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
+                ok = __all_sync(FULL, rows_wait(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
                 if (!ok) break;
                 tc::fence_after();
                 // the V rows that a partly visible tile has to be rid of (below)
@@ -713,7 +748,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     // rows that not everybody sees set aside (with two query tiles
                     // PV_B follows PV_A, which waits for these warps)
                     const uint32_t sv = st + rows_v_place(fold, j, n);
-                    ok = __all_sync(FULL, dev::mbar_wait_bounded(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns));
+                    ok = __all_sync(FULL, rows_wait(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns));
                     if (!ok) break;
                     const uint32_t vt = ring + (sv % NS) * C::TILE_BYTES;
                     const bool paged = a.block_table && !is_new;
@@ -738,14 +773,9 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     if (lane == 0) dev::mbar_arrive(p_full + 8 * x);
                     continue;
                 }
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc::tmem_ld32(s_t + 32 * q, sr[q]);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc::reg_fence(sr[q]);
-                if (partial) {  // the keys of the tile that this row sees
-                    uint32_t w[4];
+                // the columns that this row does not see
+                uint32_t w[4];
+                if (partial) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (!is_new)
@@ -757,18 +787,37 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         else
                             w[q] = lead_word(min(nv, t - key0 + 1), q);
                     }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(w[q] >> e & 1u)) sr[q][e] = __float_as_uint(-INFINITY);
                 }
+                // two halves of the scores: the first one's maximum is taken while
+                // the second is on its way from tensor memory
+                uint32_t sr[4][32];
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tc::tmem_ld32(s_t, sr[0]);
+                tc::tmem_ld32(s_t + 32, sr[1]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int hh = 0; hh < 2; ++hh) {
+                    tc::tmem_ld_wait();
+                    tc::reg_fence(sr[2 * hh]);
+                    tc::reg_fence(sr[2 * hh + 1]);
+                    if (hh == 0) {
+                        tc::tmem_ld32(s_t + 64, sr[2]);
+                        tc::tmem_ld32(s_t + 96, sr[3]);
+                    }
+                    if (partial) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        m4[q] = fmax3(m4[q], __uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                        for (int q = 2 * hh; q < 2 * hh + 2; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(w[q] >> e & 1u)) sr[q][e] = __float_as_uint(-INFINITY);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+#pragma unroll
+                        for (int q = 2 * hh; q < 2 * hh + 2; ++q) {
+                            m4[2 * (q & 1)] = fmax3(m4[2 * (q & 1)], __uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+                            m4[2 * (q & 1) + 1] = fmax3(m4[2 * (q & 1) + 1], __uint_as_float(sr[q][e + 2]), __uint_as_float(sr[q][e + 3]));
+                        }
+                }
                 // (a TMEM lane without a query row: whatever it holds stays in its lane)
                 const float m_tile = row_ok ? fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * a.scale_log2 : -INFINITY;
                 const float m_new = m_tile > m_run + C::RESCALE_LOG2 ? m_tile : m_run;
@@ -821,7 +870,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (fold && x == 0) {
                 // stream B reads both accumulators (and lets them go; those of the
                 // item before, too, before its values here are overwritten)
-                ok = k == 0 || __all_sync(FULL, dev::mbar_wait_bounded(o_free, uint32_t(k - 1) & 1, flags, a.timeout_ns));
+                ok = k == 0 || __all_sync(FULL, rows_wait(o_free, uint32_t(k - 1) & 1, flags, a.timeout_ns));
                 if (!ok) break;
                 fold_ml[r] = make_float2(m_run, l);
                 __syncwarp();
@@ -830,10 +879,10 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 leave();
                 continue;
             }
-            ok = dev::mbar_wait_bounded(o_full + 8 * x, gi & 1, flags, a.timeout_ns);
+            ok = rows_wait(o_full + 8 * x, gi & 1, flags, a.timeout_ns);
             if (fold) {  // (stream A has a part in every item: its phase is k's)
-                ok = ok && dev::mbar_wait_bounded(fold_bar, folds & 1, flags, a.timeout_ns) &&
-                     dev::mbar_wait_bounded(o_full, uint32_t(k) & 1, flags, a.timeout_ns);
+                ok = ok && rows_wait(fold_bar, folds & 1, flags, a.timeout_ns) &&
+                     rows_wait(o_full, uint32_t(k) & 1, flags, a.timeout_ns);
                 ++folds;
             }
             ok = __all_sync(FULL, ok);
@@ -861,53 +910,59 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 }
             };
             if (it.slot < 0 && !any_odd) {
-                // the whole item: fragments of 16 query rows x 32 columns at a time,
-                // so that four lanes hold 32 columns of a row and, transposed,
-                // write 64 contiguous bytes (a row per lane, 16 bytes at a time,
-                // keeps the store path busy four times as long, and with it
-                // every barrier of the CTA)
-                const int quad = lane >> 2, ql = lane & 3;
-                T *rows_out[4];  // query rows 8 i + quad of the warp's 32
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rr = 32 * qd + 8 * i + quad, rt = rr / G, tok = qx * TB + rt;
-                    rows_out[i] = rt < TB && tok < it.ntok
-                                      ? reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + (rr - rt * G), it.t0 + tok, D) + 8 * ql
-                                      : nullptr;
-                }
-                // a row of zeros where nothing was seen (whatever the accumulator holds)
+                // the whole item, as fragments of 16 query rows x D columns: four
+                // lanes hold 32 columns of a row and, transposed, write 64
+                // contiguous bytes (a row per lane, 16 bytes at a time, would keep
+                // the store path busy four times as long).  A row of zeros where
+                // nothing was seen, whatever the accumulator holds
                 const float g_b = l > 0.f ? f_b * inv : 0.f, g_a = l > 0.f ? f_a * inv : 0.f;
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t o[16], oa[16];
-                        const uint32_t at = o_t + (uint32_t(16 * h) << 16) + 32 * q;
-                        rows_tmem_ld_frag(at, o);
-                        if (fold) rows_tmem_ld_frag(at - D, oa);
-                        tc::tmem_ld_wait();
-                        rows_reg_fence16(o);
-                        if (fold) rows_reg_fence16(oa);
-                        if (q == D / 32 - 1 && h == 1) release();
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[D / 32][16];
+                    const uint32_t at = o_t + (uint32_t(16 * h) << 16);
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) rows_tmem_ld_frag(at + 32 * q, o[q]);
+                    float gb[2], ga[2];
+                    T *to[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        gb[i] = __shfl_sync(FULL, g_b, 16 * h + 8 * i + (lane >> 2));
+                        ga[i] = __shfl_sync(FULL, g_a, 16 * h + 8 * i + (lane >> 2));
+                        const int tok = qx * TB + frag_tok[2 * h + i];
+                        to[i] = frag_tok[2 * h + i] < TB && tok < it.ntok
+                                    ? reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + frag_head[2 * h + i], it.t0 + tok, D) + 8 * (lane & 3)
+                                    : nullptr;
+                    }
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) rows_reg_fence16(o[q]);
+                    if (fold) {
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t oa[16];
+                            rows_tmem_ld_frag(at - D + 32 * q, oa);
+                            tc::tmem_ld_wait();
+                            rows_reg_fence16(oa);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int i = (e >> 1) & 1;
+                                o[q][e] = __float_as_uint(fmaf(__uint_as_float(o[q][e]), gb[i], __uint_as_float(oa[e]) * ga[i]));
+                            }
+                        }
+                        gb[0] = gb[1] = 1.f;
+                    }
+                    if (h == 1) release();
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int src = 16 * h + 8 * i + quad;
-                            const float gb = __shfl_sync(FULL, g_b, src), ga = __shfl_sync(FULL, g_a, src);
                             uint32_t w[4];
 #pragma unroll
-                            for (int n4 = 0; n4 < 4; ++n4) {
-                                float y0 = __uint_as_float(o[4 * n4 + 2 * i]) * gb, y1 = __uint_as_float(o[4 * n4 + 2 * i + 1]) * gb;
-                                if (fold) {
-                                    y0 = fmaf(__uint_as_float(oa[4 * n4 + 2 * i]), ga, y0);
-                                    y1 = fmaf(__uint_as_float(oa[4 * n4 + 2 * i + 1]), ga, y1);
-                                }
-                                w[n4] = Ops::pack(y0, y1);
-                            }
+                            for (int n4 = 0; n4 < 4; ++n4)
+                                w[n4] = Ops::pack(__uint_as_float(o[q][4 * n4 + 2 * i]) * gb[i], __uint_as_float(o[q][4 * n4 + 2 * i + 1]) * gb[i]);
                             rows_quad_transpose(w, lane);
-                            T *to = rows_out[2 * h + i];
-                            if (to) *reinterpret_cast<uint4 *>(to + 32 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (to[i]) *reinterpret_cast<uint4 *>(to[i] + 32 * q) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    }
                 }
                 leave();
                 continue;
@@ -987,12 +1042,12 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     // after an abort, wait (bounded) for the copies that may still land
     if (warp == C::ITEM_WARP && lane == 0 && flags[0] && queries > 0) {
         const volatile int never = 0;
-        dev::mbar_wait_bounded(q_full, uint32_t(queries - 1) & 1, &never, a.timeout_ns);
+        rows_wait(q_full, uint32_t(queries - 1) & 1, &never, a.timeout_ns);
     }
     if (warp == C::K_WARP && lane == 0 && flags[0]) {
         const volatile int never = 0;
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-            dev::mbar_wait_bounded(full + 8 * (i % NS), uint32_t(i / NS) & 1, &never, a.timeout_ns);
+            rows_wait(full + 8 * (i % NS), uint32_t(i / NS) & 1, &never, a.timeout_ns);
     }
 }
 
