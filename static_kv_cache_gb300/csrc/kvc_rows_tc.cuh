@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 if (k >= 2) ok = __all_sync(FULL, rows_wait(item_empty + 8 * (k & 1), uint32_t((k >> 1) - 1) & 1, flags, a.timeout_ns));
                 if (!ok) break;
                 if (lane == 0) {
+                    odd[k & 3] = 0;  // (every role has left item k - 2)
                     *reinterpret_cast<RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1)) = it;
                     dev::mbar_arrive(item_full + 8 * (k & 1));
                 }
@@ -724,8 +725,6 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 continue;
             }
             const int qx = two ? x : 0;  // query tile of this stream
-            // (the slot of item k - 3, which every role has left: item k is there)
-            if (threadIdx.x == 0) odd[(k + 1) & 3] = 0;
             const int t = it.t0 + qx * TB + tt;              // token
             const bool row_ok = tt < TB && qx * TB + tt < it.ntok;
             const bool warp_ok = __any_sync(FULL, row_ok);  // else the warp's lanes hold no query row
@@ -820,43 +819,53 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 }
                 // (a TMEM lane without a query row: whatever it holds stays in its lane)
                 const float m_tile = row_ok ? fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * a.scale_log2 : -INFINITY;
-                const float m_new = m_tile > m_run + C::RESCALE_LOG2 ? m_tile : m_run;
-                const float corr = m_new == m_run ? 1.f : ex2_approx(m_run - m_new);
-                m_run = m_new;
-                const float negm = m_run == -INFINITY ? 0.f : -m_run;
-                const float2 neg2 = make_float2(negm, negm);
-                if (j > j_first && __any_sync(FULL, corr != 1.f)) {
-                    // PV of the tile before is done (it precedes this S), the next waits for P
+                if (__any_sync(FULL, m_tile > m_run + C::RESCALE_LOG2)) {
+                    const float m_new = m_tile > m_run + C::RESCALE_LOG2 ? m_tile : m_run;
+                    const float corr = m_new == m_run ? 1.f : ex2_approx(m_run - m_new);
                     const float2 c2 = make_float2(corr, corr);
+                    m_run = m_new;
+                    l2 = __fmul2_rn(l2, c2);
+                    if (j > j_first) {
+                        // PV of the tile before is done (it precedes this S), the next waits for P
 #pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t o[16];
-                        rows_tmem_ld16(o_t + 16 * q, o);
-                        tc::tmem_ld_wait();
-                        rows_reg_fence16(o);
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t o[16];
+                            rows_tmem_ld16(o_t + 16 * q, o);
+                            tc::tmem_ld_wait();
+                            rows_reg_fence16(o);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), c2);
-                            o[e] = __float_as_uint(y.x);
-                            o[e + 1] = __float_as_uint(y.y);
+                            for (int e = 0; e < 16; e += 2) {
+                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), c2);
+                                o[e] = __float_as_uint(y.x);
+                                o[e + 1] = __float_as_uint(y.y);
+                            }
+                            rows_tmem_st16(o_t + 16 * q, o);
                         }
-                        rows_tmem_st16(o_t + 16 * q, o);
                     }
                 }
-                float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float negm = m_run == -INFINITY ? 0.f : -m_run;
+                const float2 neg2 = make_float2(negm, negm);
+                float2 ps[4] = {l2, make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1])), scale2, neg2);
+                        sr[q][e] = __float_as_uint(y.x);
+                        sr[q][e + 1] = __float_as_uint(y.y);
+                    }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1])), scale2, neg2);
-                        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                        const float p0 = ex2_approx(__uint_as_float(sr[q][e])), p1 = ex2_approx(__uint_as_float(sr[q][e + 1]));
                         ps[(e >> 1) & 3] = __fadd2_rn(ps[(e >> 1) & 3], make_float2(p0, p1));
                         pk[e / 2] = Ops::pack(p0, p1);
                     }
                     rows_tmem_st16(s_t + 16 * q, pk);  // over scores that are in registers
                 }
-                l2 = __ffma2_rn(l2, make_float2(corr, corr), __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3])));
+                l2 = __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
                 tc::tmem_st_wait();
                 tc::fence_before();
                 __syncwarp();
