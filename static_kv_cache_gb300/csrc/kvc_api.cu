@@ -272,10 +272,10 @@ bool kvc::encode_pool_head_maps(int32_t dtype, int D, int H_kv, int64_t blocks_t
     if (!encode || (dtype != KVC_BF16 && dtype != KVC_FP16) || D % 64 != 0) return false;
     const CUtensorMapDataType dt = dtype == KVC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t row = cuuint64_t(D) * 2;  // bytes of one row
-    const cuuint64_t dims[5] = {64, 16, cuuint64_t(D / 64), cuuint64_t(H_kv), cuuint64_t(blocks_total)};
-    const cuuint64_t strides[4] = {row, 128, 16 * row, cuuint64_t(H_kv) * 16 * row};
+    const cuuint64_t dims[5] = {64, 8, cuuint64_t(D / 64), 2, cuuint64_t(blocks_total) * H_kv};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, 16 * row};
     const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
-    const cuuint32_t box[5] = {64, 16, cuuint32_t(D / 64), 1, 1};
+    const cuuint32_t box[5] = {64, 8, cuuint32_t(D / 64), 2, 1};
     const void *bases[2] = {k_pool, v_pool};
     CUtensorMap *outs[2] = {k, v};
     for (int i = 0; i < 2; ++i)

@@ -263,10 +263,10 @@ cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, int smem, cudaStrea
 // them (its first 8 rows), 128-byte swizzle.  Host only.
 bool encode_pool_maps(int32_t dtype, int D, int64_t n_blocks_total, const void *k_pool, const void *v_pool,
                       CUtensorMap *k16, CUtensorMap *k8, CUtensorMap *v16, CUtensorMap *v8);
-// Tensor maps of paged pools as 5-D arrays (64 columns, 16 rows, D/64 column
-// blocks, H_kv heads, blocks_total = L * num_blocks blocks), 128-byte swizzle:
-// boxes of (64, 16, D/64, 1, 1), the block's rows of one KV head laid out column
-// block after column block.  Host only.
+// Tensor maps of paged pools as 5-D arrays (64 columns, 8 rows, D/64 column
+// blocks, 2 half blocks, blocks_total * H_kv rows of blocks of one KV head;
+// blocks_total = L * num_blocks), 128-byte swizzle: boxes of all but the last
+// dimension, a block's rows of one KV head.  Host only.
 bool encode_pool_head_maps(int32_t dtype, int D, int H_kv, int64_t blocks_total, const void *k_pool,
                            const void *v_pool, CUtensorMap *k, CUtensorMap *v);
 // Tensor maps of paged pools read two KV heads at a time: the pools as 5-D

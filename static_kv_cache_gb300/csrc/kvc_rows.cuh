@@ -80,10 +80,11 @@ struct RowsTcArgs : RowsArgs {
     int32_t item_cost;           // an item's start and end, in key tiles
     int32_t min_share;           // length of a CTA's share of the line, at least
     int32_t split_min;           // items of at most so many key tiles are not cut
-    int32_t seg_base;            // tensor-map segment (block) of the layer's first: layer * B * H_kv (layer * num_blocks)
-    int32_t pool_end;            // paged: one past the map's last block
+    int32_t seg_base;            // tensor-map segment of the layer's first: layer * B * H_kv (paged: layer * num_blocks * H_kv)
+    int32_t pool_end;            // paged: one past the map's last segment
+    int32_t read_once;           // every (sequence, KV head) is one item: its cached rows are read once
     unsigned long long timeout_ns;
-    CUtensorMap tm_k, tm_v;          // the cache: (D, T_max, segments) or the pool: (64, 16, D / 64, H_kv, blocks)
+    CUtensorMap tm_k, tm_v;          // the cache: (D, T_max, segments) or the pool: (64, 8, D / 64, 2, H_kv blocks)
     CUtensorMap tm_k_new, tm_v_new;  // new rows: (D, H_kv, total) packed, (D, T, B H_kv) dense
     CUtensorMap tm_q;                // (D, H, total) packed, (D, H, T, B) dense: boxes of 64 columns, g heads, 128 / g tokens
 };

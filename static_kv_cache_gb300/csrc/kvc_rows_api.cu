@@ -80,8 +80,8 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
         return KVC_ERR_CUDA;
     a.tm_k = h->rows_k;
     a.tm_v = h->rows_v;
-    a.seg_base = layer * (h->block_table ? h->num_blocks : c.batch * c.n_kv_heads);
-    a.pool_end = c.n_layers * h->num_blocks;
+    a.seg_base = layer * (h->block_table ? h->num_blocks : c.batch) * c.n_kv_heads;
+    a.pool_end = c.n_layers * h->num_blocks * c.n_kv_heads;
     a.timeout_ns = kvc::WAIT_TIMEOUT_NS;
     uint64_t ml, acc;
     kvc::rows_workspace(c.d_head, &ml, &acc);
@@ -94,16 +94,19 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     const int64_t item = (max_cached + 127) / 128 + (int64_t(max_tokens) + 127) / 128;
     const int64_t blocks = r.cu_seqlens ? r.total / ti + (c.batch < r.total ? c.batch : r.total)
                                         : int64_t(c.batch) * ((r.T + ti - 1) / ti);
+    a.read_once = !r.cu_seqlens && r.T <= ti;
     a.item_cost = 2;
-    a.min_share = 4 + a.item_cost;
-    a.split_min = item > 4 ? 4 : 0x7fffffff;  // (nothing is cut where no combine follows)
+    // An item of up to 8 key tiles takes about as long as its pieces' combine.
+    constexpr int SHORT = 8;
+    a.min_share = 4;
+    a.split_min = item > SHORT ? SHORT : 0x7fffffff;  // (nothing is cut where no combine follows)
     const int64_t line = blocks * c.n_kv_heads * (item + a.item_cost);
     if (line > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     int64_t grid = h->num_sms < kvc::ROWS_MAX_CTAS ? h->num_sms : kvc::ROWS_MAX_CTAS;
     if ((line + a.min_share - 1) / a.min_share < grid) grid = (line + a.min_share - 1) / a.min_share;
     // the query tiles an item can fill
     const int rows = max_tokens >= ti ? 256 : max_tokens > ti / 2 ? 128 + (max_tokens - ti / 2) * h->group : max_tokens * h->group;
-    const cudaError_t e = h->rows->launch(a, int(grid), item > 4 ? rows : 0, s);
+    const cudaError_t e = h->rows->launch(a, int(grid), item > SHORT ? rows : 0, s);
     return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

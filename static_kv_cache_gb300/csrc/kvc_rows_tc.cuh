@@ -38,11 +38,10 @@
 // (one ring, in the order in which the MMAs take them); 9 issues the MMAs and
 // owns tensor memory; 10 walks the items, hands them to the others and copies
 // their query rows.  Cached rows of a contiguous cache and new rows come as
-// boxes of 128 rows x 64 columns.  A page of 16 rows comes as one box of 16 rows
-// x d_h columns, laid out column block after column block: for d_h = 128 the
-// eight-row groups of a tile then lie 4096 bytes apart, so S takes the tile as
-// two MMAs of 64 keys (the upper and the lower halves of the eight pages) and
-// the score columns are in that order.
+// boxes of 128 rows x 64 columns.  A page of 16 rows (of one KV head) comes as one
+// box of half pages x column blocks x 8 rows x 64 columns: the eight-row groups
+// of a column block then lie 2048 bytes apart (d_h = 128) across all pages of a
+// tile, which the MMA's descriptors take as they are.
 //
 // A tile that is not full holds foreign rows behind its own: their scores are
 // masked, and their V rows are zeroed in shared memory before the PV (0 times
@@ -96,9 +95,9 @@ struct RowsTcCfg {
     __device__ __forceinline__ static uint32_t swz(uint32_t tile, int r, int c) {
         return tile + uint32_t(c >> 3) * BLK + uint32_t(r) * 128 + (uint32_t((c & 7) ^ (r & 7)) << 4);
     }
-    // the same for a tile of eight pages, each laid out column block after column block
+    // the same for a tile of eight pages, each as half pages of CB column blocks of eight rows
     __device__ __forceinline__ static uint32_t swz_paged(uint32_t tile, int r, int c) {
-        return tile + uint32_t(r >> 4) * (CB * 2048) + uint32_t(c >> 3) * 2048 + uint32_t(r & 15) * 128 +
+        return tile + uint32_t(r >> 3) * (CB * 1024) + uint32_t(c >> 3) * 1024 + uint32_t(r & 7) * 128 +
                (uint32_t((c & 7) ^ (r & 7)) << 4);
     }
 };
@@ -315,17 +314,6 @@ __device__ __forceinline__ uint32_t lead_word(int lim, int k) {
     const int m = lim - 32 * k;
     return m >= 32 ? 0xffffffffu : m <= 0 ? 0u : (1u << m) - 1u;
 }
-// The same where the columns are the upper, then the lower halves of eight pages.
-__device__ __forceinline__ uint32_t lead_word_paged(int lim, int k) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int m = lim - (((4 * k + e) & 7) * 16 + (k >> 1) * 8);
-        w |= (m >= 8 ? 0xffu : m <= 0 ? 0u : (1u << m) - 1u) << (8 * e);
-    }
-    return w;
-}
-
 // Infinities and NaN among the eight 16-bit elements of a vector.
 template <typename T>
 __device__ __forceinline__ bool not_finite(const uint4 &v) {
@@ -367,7 +355,6 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     constexpr unsigned FULL = 0xffffffffu;
     constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t IDESC_S = tc::idesc_f16_f32acc(BF16, 128, BN, false, false);
-    constexpr uint32_t IDESC_S64 = tc::idesc_f16_f32acc(BF16, 128, 64, false, false);
     constexpr uint32_t IDESC_O = tc::idesc_f16_f32acc(BF16, 128, D, false, true);
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -504,6 +491,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (!ok) give_up();
         } else if (warp == C::K_WARP) {
             // ------------------------------------------------------------ K and V copies
+            // cached rows that one item reads leave L2 to what is read again
+            const uint64_t pol = a.read_once ? dev::l2_evict_first_policy() : dev::l2_evict_normal_policy();
             bool ok = true;
             RowsItem it;
             for (int k = 0; ok; ++k) {
@@ -551,7 +540,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                                 const CUtensorMap *m = v ? &a.tm_v : &a.tm_k;
 #pragma unroll
                                 for (int cb = 0; cb < CB; ++cb)
-                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * j, a.seg_base + it.b * a.H_kv + it.kv, bar);
+                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * j, a.seg_base + it.b * a.H_kv + it.kv, bar, pol);
                             }
                         } else {
                             // the pages that hold cached rows, one lane each; a page out of
@@ -562,8 +551,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                             if (lane < pages) {
                                 const bool in = page >= 0 && page < a.num_blocks;
                                 if (!in) dev::record_error(a.err, ERR_DEVICE_INDEX);
-                                dev::tma_load_5d(dst + lane * (CB * 2048), v ? &a.tm_v : &a.tm_k, 0, 0, 0, it.kv,
-                                                 in ? a.seg_base + page : a.pool_end, bar);
+                                dev::tma_load_5d(dst + lane * (CB * 2048), v ? &a.tm_v : &a.tm_k, 0, 0, 0, 0,
+                                                 in ? a.seg_base + page * a.H_kv + it.kv : a.pool_end, bar, pol);
                             }
                         }
                         ++issued;
@@ -578,7 +567,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             // Tiles are taken in ring order, ahead of the wait for P: what stands
             // between that wait and the MMAs is idle time of the tensor cores.
             const bool leader = rows_elect();
-            constexpr uint32_t HI1 = rows_desc_hi(1024), HI4 = rows_desc_hi(4096);
+            constexpr uint32_t HI1 = rows_desc_hi(1024), HI2 = rows_desc_hi(2048);
             bool ok = true;
             RowsItem it;
             uint32_t stage = 0, phase = 0;                                   // next tile of the ring
@@ -594,11 +583,9 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 if (leader) {
                     if (CB == 2 && paged) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks)
-                                tc::mma_f16_ss(s_t + 64 * h, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
-                                               rows_desc(kt + (((ks >> 2) * 2048 + (ks & 3) * 32 + h * 1024) >> 4), HI4), IDESC_S64, ks > 0);
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            tc::mma_f16_ss(s_t, rows_desc(qt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1),
+                                           rows_desc(kt + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), HI2), IDESC_S, ks > 0);
                     } else {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
@@ -614,7 +601,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     if (CB == 2 && paged) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + (((ks & 3) * 8192 + (ks >> 2) * 1024) >> 4) + ((2048 >> 4) << 16), HI4),
+                            tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 4096) >> 4) + ((1024 >> 4) << 16), HI2),
                                            IDESC_O, ks > 0 || !first);
                     } else {
 #pragma unroll
@@ -778,7 +765,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (!is_new)
-                            w[q] = CB == 2 && a.block_table ? lead_word_paged(nv, q) : lead_word(nv, q);
+                            w[q] = lead_word(nv, q);
                         else if (a.tree_mask)
                             w[q] = row_ok && key0 / 32 + q < a.mask_words
                                        ? __ldg(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + key0 / 32 + q) & lead_word(nv, q)
