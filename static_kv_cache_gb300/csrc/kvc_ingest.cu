@@ -129,55 +129,72 @@ __global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constan
     }
 }
 
-// A warp takes eight path positions of one (layer, K or V, sequence, KV head).
+// A warp takes eight path positions of one (layer, sequence, KV head), K and V:
+// one lane each looks up a position's source and destination, then every row
+// moves with four vectors of K and four of V in flight per lane.
 constexpr int STEPS = 8;
 
 template <bool INT8>
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ IngestArgs a) {
     dev::grid_dependency_wait();
     dev::allow_dependents();
-    const int lane = threadIdx.x & 31;
-    const int chunks = (a.P + STEPS - 1) / STEPS;
-    const int64_t segs = int64_t(a.B) * a.H_kv, units = 2 * segs * a.n_layers * chunks;
-    for (int64_t u = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 8) {
-        const int64_t w = u / chunks;
-        const int chunk = int(u - w * chunks);
-        const bool is_v = w & 1;
-        const int64_t ls = w >> 1;                 // layer * segs + seg
-        const int layer = int(ls / segs), seg = int(ls - layer * segs), b = seg / a.H_kv, kv = seg - b * a.H_kv;
-        const int n = __ldg(a.n_accept + b), c = __ldg(a.cache_index + b);
-        bool bad = n < 0 || n > a.P || c < 0 || c > a.max_ctx || n > a.max_ctx - c;
-        if (!bad) {
-            for (int i = lane; i < n; i += 32) {
-                const int s = __ldg(a.path + int64_t(b) * a.P + i);
-                bad = bad || s < 0 || s >= a.T;
-            }
-            bad = __any_sync(0xffffffffu, bad);
+    const int lane = threadIdx.x & 31, layer = blockIdx.y;
+    const unsigned chunks = unsigned(a.P + STEPS - 1) / STEPS, segs = unsigned(a.B) * a.H_kv;
+    const unsigned u = blockIdx.x * 8 + (threadIdx.x >> 5);  // (sequence, KV head, chunk)
+    if (u >= segs * chunks) return;
+    const unsigned seg = u / chunks, chunk = u - seg * chunks, b = seg / a.H_kv, kv = seg - b * a.H_kv;
+    const int n = __ldg(a.n_accept + b), c = __ldg(a.cache_index + b), i0 = int(chunk) * STEPS;
+    bool bad = n < 0 || n > a.P || c < 0 || c > a.max_ctx || n > a.max_ctx - c;
+    if (!bad && (i0 < n || chunk == 0)) {
+        for (int i = lane; i < n; i += 32) {
+            const int s = __ldg(a.path + int64_t(b) * a.P + i);
+            bad = bad || s < 0 || s >= a.T;
         }
-        if (bad) {
-            if (u == int64_t(b) * a.H_kv * 2 * chunks && lane == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
-            continue;
+        bad = __any_sync(0xffffffffu, bad);
+    }
+    if (bad) {
+        if (chunk == 0 && kv == 0 && layer == 0 && lane == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
+        return;
+    }
+    const int steps = min(STEPS, n - i0);
+    if (steps <= 0) return;
+    int64_t to = -1, from = 0;  // lane i: row of position i0 + i in the cache and in k_new / v_new
+    if (lane < steps) {
+        int64_t row, step;
+        from = (int64_t(layer) * segs + seg) * a.T + __ldg(a.path + int64_t(b) * a.P + i0 + lane);
+        if (cache_row(a, b, c + i0 + lane, row, step))
+            to = row + kv * step;
+        else
+            dev::record_error(a.err, ERR_DEVICE_INDEX);
+    }
+    uint8_t *K = a.K + layer * a.layer_bytes, *V = a.V + layer * a.layer_bytes;
+    if constexpr (INT8) {
+        for (int i = 0; i < steps; ++i) {
+            const int64_t d = __shfl_sync(0xffffffffu, to, i), f = __shfl_sync(0xffffffffu, from, i);
+            store_q8<128>(a.k_new + f * 256, K + d * 128, a.k_scale + layer * a.layer_scales + d, lane);
+            store_q8<128>(a.v_new + f * 256, V + d * 128, a.v_scale + layer * a.layer_scales + d, lane);
         }
-        const uint8_t *src = (is_v ? a.v_new : a.k_new) + ls * a.T * a.row_vecs * 16;
-        uint8_t *dst = (is_v ? a.V : a.K) + layer * a.layer_bytes;
-        const int i0 = chunk * STEPS, steps = min(STEPS, n - i0);
-        if constexpr (INT8) {
-            float *sc = (is_v ? a.v_scale : a.k_scale) + layer * a.layer_scales;
-            for (int i = i0; i < i0 + steps; ++i) {
-                const int64_t row = int64_t(seg) * a.max_ctx + c + i;
-                store_q8<128>(src + int64_t(__ldg(a.path + int64_t(b) * a.P + i)) * 256, dst + row * 128, sc + row, lane);
-            }
-        } else {
-            for (int x = lane; x < steps * a.row_vecs; x += 32) {
-                const int i = i0 + x / a.row_vecs, v = x % a.row_vecs;
-                int64_t row, step;
-                if (!cache_row(a, b, c + i, row, step)) {
-                    dev::record_error(a.err, ERR_DEVICE_INDEX);
-                    continue;
+    } else {
+        const int vecs = steps * a.row_vecs;
+        for (int x0 = 0; x0 < vecs; x0 += 128) {
+            uint4 k[4], v[4];
+            int64_t at[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int x = x0 + 32 * e + lane, i = min(x / a.row_vecs, steps - 1), w = x % a.row_vecs;
+                const int64_t d = __shfl_sync(0xffffffffu, to, i), f = __shfl_sync(0xffffffffu, from, i);
+                at[e] = x < vecs && d >= 0 ? d * a.row_vecs + w : -1;
+                if (at[e] >= 0) {
+                    k[e] = __ldg(reinterpret_cast<const uint4 *>(a.k_new) + f * a.row_vecs + w);
+                    v[e] = __ldg(reinterpret_cast<const uint4 *>(a.v_new) + f * a.row_vecs + w);
                 }
-                const int64_t from = int64_t(__ldg(a.path + int64_t(b) * a.P + i)) * a.row_vecs + v;
-                reinterpret_cast<uint4 *>(dst)[(row + kv * step) * a.row_vecs + v] = __ldg(reinterpret_cast<const uint4 *>(src) + from);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (at[e] >= 0) {
+                    reinterpret_cast<uint4 *>(K)[at[e]] = k[e];
+                    reinterpret_cast<uint4 *>(V)[at[e]] = v[e];
+                }
         }
     }
 }
@@ -196,9 +213,10 @@ cudaError_t launch_append_packed(const IngestArgs &a, bool int8, int num_sms, cu
                 : launch_pdl(append_packed_kernel<false>, grid, dim3(256), 0, s, a);
 }
 
-cudaError_t launch_tree_commit(const IngestArgs &a, bool int8, int num_sms, cudaStream_t s) {
-    const int64_t units = 2ll * a.B * a.H_kv * a.n_layers * ((a.P + STEPS - 1) / STEPS);
-    const dim3 grid(grid_of((units + 7) / 8, num_sms));
+cudaError_t launch_tree_commit(const IngestArgs &a, bool int8, cudaStream_t s) {
+    const int64_t units = int64_t(a.B) * a.H_kv * ((a.P + STEPS - 1) / STEPS);
+    if (units > 0x7fffffff || a.n_layers > 65535) return cudaErrorInvalidValue;
+    const dim3 grid(unsigned((units + 7) / 8), unsigned(a.n_layers));
     return int8 ? launch_pdl(tree_commit_kernel<true>, grid, dim3(256), 0, s, a)
                 : launch_pdl(tree_commit_kernel<false>, grid, dim3(256), 0, s, a);
 }

@@ -31,7 +31,7 @@ struct PagesArgs {
     // workspace: the number of copies, then their (src, dst, rows)
     int32_t *n_copies, *src, *dst, *rows;
     int32_t *list;         // [num_blocks]: blocks in hand-out (or moving) order
-    int32_t *where;        // [num_blocks]: reserve, their logical blocks; compact, where each block goes
+    int32_t *where;        // [num_blocks]: reserve, the places they go to; compact, where each block goes
 };
 
 // An entry as the calls take it: a block, or -1 (anything else is recorded).
@@ -119,89 +119,102 @@ __device__ __forceinline__ int block_scan(int x, int *part, int &all) {
 }
 
 // ---- reserve ----------------------------------------------------------------
-// Which pages of its range [len / 16, ceil(new_len / 16)) sequence b has to
-// have replaced or added.  A shared page: of its holders that reserve it in
+// The range of sequence b is its logical blocks [len / 16, ceil(new_len / 16)):
+// pages missing there are added, shared ones replaced.  A shared page: of its holders that reserve it in
 // this call the first ones (by sequence) leave it while its count is above 1.
 struct Reserve {
     const int32_t *len, *new_len;
 };
 
-__device__ __forceinline__ bool range_of(const PagesArgs &a, const Reserve &r, int b, int &len, int &j0, int &j1) {
-    len = __ldg(r.len + b);
-    const int grown = __ldg(r.new_len + b);
-    if (len < 0 || grown < len || grown > a.max_ctx) return false;
-    j0 = len / PAGE;
-    j1 = grown > len ? (grown + PAGE - 1) / PAGE : j0;
-    return true;
-}
-
-// Does sequence b need a fresh page at logical block j of its range?
-__device__ __forceinline__ bool wants(const PagesArgs &a, const uint32_t *ranges, int b, int j) {
-    const int x = a.table[int64_t(b) * a.max_blocks + j];
+// Does sequence b need a fresh page at logical block j of its range, which is x
+// now?
+__device__ __forceinline__ bool wants(const PagesArgs &a, const int32_t *first, const int32_t *offset, int b, int j, int x) {
     if (x < 0 || x >= a.num_blocks) return true;
     int held = a.refs[x];
     if (held <= 1) return false;
     for (int k = 0; k < b; ++k)  // earlier holders that leave it
-        if (int(ranges[2 * k]) <= j && j < int(ranges[2 * k + 1]) && a.table[int64_t(k) * a.max_blocks + j] == x) --held;
+        if (first[k] <= j && j < first[k] + offset[k + 1] - offset[k] && a.table[int64_t(k) * a.max_blocks + j] == x) --held;
     return held > 1;
 }
 
-// One block.  need[b]: fresh pages of sequence b; then their places in the
-// order of hand-out, the lowest free blocks, and only if they suffice the
-// changes.
+// One block of 1024 threads.  The logical blocks of all ranges, sequence after
+// sequence, are one list of places; a prefix sum over the places that want a
+// page gives each its number in the order of hand-out, another one over the
+// counts finds the lowest free blocks.  Only if those suffice is anything changed.
 __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ PagesArgs a, const Reserve r) {
-    extern __shared__ uint32_t dyn[];
-    uint32_t *ranges = dyn;                                 // [B][2]: first and last + 1 logical block
-    int32_t *start = reinterpret_cast<int32_t *>(dyn + 2 * a.B);  // [B]: need, then the first place
+    extern __shared__ int32_t dyn[];
+    int32_t *first = dyn, *offset = dyn + a.B;  // [B] first logical block, [B + 1] first place
     __shared__ int part[32];
     __shared__ int copies;
     dev::grid_dependency_wait();
     dev::allow_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
+    int4 count4 = make_int4(1, 1, 1, 1);  // the first 4096 counts: on their way meanwhile
+    if (4 * tid + 3 < a.num_blocks) count4 = *reinterpret_cast<const int4 *>(a.refs + 4 * tid);
     if (tid == 0) copies = 0;
-    for (int b = tid; b < a.B; b += 1024) {
-        int len, j0, j1;
-        bool ok = range_of(a, r, b, len, j0, j1);
-        if (ok && j1 > j0 && len % PAGE != 0) {  // the page of the rows below len
-            const int x = a.table[int64_t(b) * a.max_blocks + j0];
-            ok = x >= 0 && x < a.num_blocks;
-        }
-        if (!ok) {
-            dev::record_error(a.err, ERR_DEVICE_INDEX);
-            j0 = j1 = 0;
-        }
-        ranges[2 * b] = j0;
-        ranges[2 * b + 1] = j1;
-    }
-    __syncthreads();
-    for (int b = warp; b < a.B; b += 32) {
-        int n = 0;
-        for (int j = int(ranges[2 * b]) + lane; j < int(ranges[2 * b + 1]); j += 32) n += wants(a, ranges, b, j);
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) start[b] = n;
-    }
-    __syncthreads();
-    int total = 0;
+    int places = 0;
     for (int b0 = 0; b0 < a.B; b0 += 1024) {
         const int b = b0 + tid;
+        int j0 = 0, length = 0;
+        if (b < a.B) {
+            const int len = __ldg(r.len + b), grown = __ldg(r.new_len + b);
+            bool ok = len >= 0 && grown >= len && grown <= a.max_ctx;
+            j0 = ok ? len / PAGE : 0;
+            if (ok && grown > len) {
+                length = (grown + PAGE - 1) / PAGE - j0;
+                if (len % PAGE != 0) {  // the page of the rows below len
+                    const int x = a.table[int64_t(b) * a.max_blocks + j0];
+                    ok = x >= 0 && x < a.num_blocks;
+                }
+            }
+            if (!ok) {
+                dev::record_error(a.err, ERR_DEVICE_INDEX);
+                length = 0;
+            }
+        }
         int all;
-        const int before = block_scan(b < a.B ? start[b] : 0, part, all);
-        if (b < a.B) start[b] = total + before;
+        const int before = places + block_scan(length, part, all);
+        if (b < a.B) first[b] = j0, offset[b] = before;
+        places += all;
+    }
+    if (tid == 0) offset[a.B] = places;
+    __syncthreads();
+    // the sequence of a place
+    auto sequence = [&](int place) {
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (offset[mid] <= place) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    };
+    int total = 0;
+    for (int p0 = 0; p0 < places; p0 += 1024) {
+        const int place = p0 + tid;
+        bool w = false;
+        if (place < places) {
+            const int b = sequence(place), j = first[b] + place - offset[b];
+            w = wants(a, first, offset, b, j, a.table[int64_t(b) * a.max_blocks + j]);
+        }
+        int all;
+        const int at = total + block_scan(w, part, all);
+        if (w && at < a.num_blocks) a.where[at] = place;
         total += all;
     }
     // the lowest `total` free blocks, in order
     int found = 0;
     for (int x0 = 0; x0 < a.num_blocks && found < total; x0 += 4096) {
         const int x = x0 + 4 * tid;
-        int free4 = 0, n = 0;
+        if (x0 > 0 && x + 3 < a.num_blocks) count4 = *reinterpret_cast<const int4 *>(a.refs + x);
+        int c[4] = {count4.x, count4.y, count4.z, count4.w};
+        if (x + 3 >= a.num_blocks)  // the end
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (x + e < a.num_blocks && a.refs[x + e] == 0) free4 |= 1 << e, ++n;
+            for (int e = 0; e < 4; ++e) c[e] = x + e < a.num_blocks ? a.refs[x + e] : 1;
         int all;
-        int at = found + block_scan(n, part, all);
+        int at = found + block_scan((c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0), part, all);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (free4 >> e & 1) {
+            if (c[e] == 0) {
                 if (at < total) a.list[at] = x + e;
                 ++at;
             }
@@ -215,36 +228,20 @@ __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ P
         }
         return;
     }
-    // Every warp lists its sequences' pages before any entry or count changes:
-    // `wants` reads both.
-    for (int b = warp; b < a.B; b += 32) {
-        int at = start[b];
-        for (int j0 = int(ranges[2 * b]); j0 < int(ranges[2 * b + 1]); j0 += 32) {
-            const int j = j0 + lane;
-            const bool w = j < int(ranges[2 * b + 1]) && wants(a, ranges, b, j);
-            const unsigned vote = __ballot_sync(0xffffffffu, w);
-            if (w) a.where[at + __popc(vote & ((1u << lane) - 1))] = j;
-            at += __popc(vote);
-        }
-    }
-    __syncthreads();
-    for (int b = warp; b < a.B; b += 32) {
-        const int first = start[b], last = b + 1 < a.B ? start[b + 1] : total;
+    for (int i = tid; i < total; i += 1024) {
+        const int place = a.where[i], page = a.list[i], b = sequence(place), j = first[b] + place - offset[b];
+        int32_t *at = a.table + int64_t(b) * a.max_blocks + j;
+        const int was = *at;
+        *at = page;
+        a.refs[page] = 1;
+        if (entry(a, was) < 0) continue;
+        atomicSub(a.refs + was, 1);
         const int len = __ldg(r.len + b);
-        for (int i = first + lane; i < last; i += 32) {
-            const int j = a.where[i], page = a.list[i];
-            int32_t *at = a.table + int64_t(b) * a.max_blocks + j;
-            const int was = *at;
-            *at = page;
-            a.refs[page] = 1;
-            if (entry(a, was) < 0) continue;
-            atomicSub(a.refs + was, 1);
-            if (j == len / PAGE && len % PAGE != 0) {  // (at most one page of a sequence)
-                const int c = atomicAdd(&copies, 1);
-                a.src[c] = was;
-                a.dst[c] = page;
-                a.rows[c] = len % PAGE;
-            }
+        if (j == len / PAGE && len % PAGE != 0) {  // (at most one page of a sequence)
+            const int c = atomicAdd(&copies, 1);
+            a.src[c] = was;
+            a.dst[c] = page;
+            a.rows[c] = len % PAGE;
         }
     }
     __syncthreads();
@@ -436,9 +433,11 @@ kvc_status kvc_pages_fork(kvc_cache *h, int32_t *block_table, int32_t *refcount,
     const kvc_status st = kvc::pages_args(h, block_table, refcount, a);
     if (st != KVC_OK) return st;
     if (!parent) return KVC_ERR_INVALID;
-    // the columns of a block's table rows: as many as 48 KB hold, at most 32
-    int cols = 48 * 1024 / (4 * a.B);
-    cols = cols > 32 ? 32 : cols < 1 ? 1 : cols;
+    // the columns of a block's table rows: four entries a thread, whole 32-byte
+    // sectors, no more than 48 KB
+    int cols = 1024 / a.B, most = 48 * 1024 / (4 * a.B);
+    cols = cols < 8 ? 8 : cols > 32 ? 32 : cols & ~7;
+    if (cols > most) cols = most < 1 ? 1 : most;
     const int grid = (a.max_blocks + cols - 1) / cols;
     return kvc::done(kvc::launch_pdl(kvc::fork_kernel, dim3(grid), dim3(256), cols * a.B * 4, static_cast<cudaStream_t>(stream),
                                      a, parent, cols));
@@ -452,9 +451,9 @@ kvc_status kvc_pages_reserve(kvc_cache *h, int32_t *block_table, int32_t *refcou
     if (!len || !new_len) return KVC_ERR_INVALID;
     st = kvc::bind_workspace(h, workspace, ws_bytes, a);
     if (st != KVC_OK) return st;
-    const int smem = 12 * a.B;
+    const int smem = 4 * (2 * a.B + 1);
     if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kvc::reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kvc::MAX_SEQS) != cudaSuccess)
+        cudaFuncSetAttribute(kvc::reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (2 * kvc::MAX_SEQS + 1)) != cudaSuccess)
         return KVC_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = kvc::launch_pdl(kvc::reserve_kernel, dim3(1), dim3(1024), smem, s, a, kvc::Reserve{len, new_len});

@@ -122,6 +122,6 @@ struct IngestArgs {
     int32_t row_vecs;            // 16-byte vectors of a row of k_new / v_new
 };
 cudaError_t launch_append_packed(const IngestArgs &a, bool int8, int num_sms, cudaStream_t s);
-cudaError_t launch_tree_commit(const IngestArgs &a, bool int8, int num_sms, cudaStream_t s);
+cudaError_t launch_tree_commit(const IngestArgs &a, bool int8, cudaStream_t s);
 
 }  // namespace kvc

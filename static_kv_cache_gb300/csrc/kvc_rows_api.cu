@@ -219,7 +219,7 @@ kvc_status kvc_tree_commit(kvc_cache *h, int32_t layer, int32_t n_layers, const 
     a.n_layers = n_layers;
     a.T = T;
     a.P = P;
-    const cudaError_t e = kvc::launch_tree_commit(a, h->cfg.dtype == KVC_INT8, h->num_sms, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = kvc::launch_tree_commit(a, h->cfg.dtype == KVC_INT8, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

@@ -555,7 +555,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                                                  in ? a.seg_base + page * a.H_kv + it.kv : a.pool_end, bar, pol);
                             }
                         }
-                        ++issued;
+                        __syncwarp();
+                    ++issued;
                     }
                 }
             }
@@ -564,6 +565,10 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             // ------------------------------------------------------------ MMAs
             // The whole warp walks the loop, one elected lane issues: the operands'
             // descriptors then stay warp-uniform, and each is its tile's plus a constant.
+            // The warp is brought together behind every wait and every issue: the
+            // instructions take their operands from registers that the warp's lanes
+            // share, and lanes that ran ahead of the issuing one would overwrite them
+            // (a commit then went to an address of nobody's).
             // Tiles are taken in ring order, ahead of the wait for P: what stands
             // between that wait and the MMAs is idle time of the tensor cores.
             const bool leader = rows_elect();
@@ -572,8 +577,9 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             RowsItem it;
             uint32_t stage = 0, phase = 0;                                   // next tile of the ring
             uint32_t tiles_a = 0, tiles_b = 0, items_a = 0, items_b = 0;     // of each stream
+            auto wait = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(FULL, ok && rows_wait(bar, parity, flags, a.timeout_ns)); };
             auto take_tile = [&]() {
-                ok = ok && rows_wait(full + 8 * stage, phase, flags, a.timeout_ns);
+                wait(full + 8 * stage, phase);
                 const uint32_t s = stage;
                 if (++stage == NS) stage = 0, phase ^= 1;
                 return s;
@@ -594,6 +600,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     }
                     tc::commit(s_full + 8 * x);
                 }
+                __syncwarp();
             };
             auto issue_pv = [&](int x, uint32_t s, bool paged, bool first) {
                 const uint32_t vt = (ring + s * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
@@ -609,9 +616,11 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                             tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 2048) >> 4) + ((BLK >> 4) << 16), HI1), IDESC_O, ks > 0 || !first);
                     }
                 }
+                __syncwarp();
             };
             auto commit_to = [&](uint32_t bar) {
                 if (leader) tc::commit(bar);
+                __syncwarp();
             };
             for (int k = 0; ok; ++k) {
                 ok = __all_sync(FULL, take_item(k, it));
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
                 const bool fold = nx == 1 && n > 1;
                 const int cached = a.block_table ? it.np - it.j0 : 0;  // the item's tiles j < cached are pages
-                ok = rows_wait(q_full, uint32_t(k) & 1, flags, a.timeout_ns);
+                wait(q_full, uint32_t(k) & 1);
                 uint32_t sk = take_tile(), sv = 0;
                 if (!ok) break;
                 tc::fence_after();
@@ -648,8 +657,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         if (jn < n) sk = take_tile();
                     }
                     const uint32_t items = x ? items_b : items_a;
-                    if (first && items > 0) ok = ok && rows_wait(o_free + 8 * x, (items - 1) & 1, flags, a.timeout_ns);
-                    ok = ok && rows_wait(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1, flags, a.timeout_ns);
+                    if (first && items > 0) wait(o_free + 8 * x, (items - 1) & 1);
+                    wait(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1);
                     if (!ok) break;
                     ++(x ? tiles_b : tiles_a);
                     tc::fence_after();
@@ -668,7 +677,6 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     }
                 }
             }
-            ok = __all_sync(FULL, ok);
             if (!ok) give_up();
             commit_to(mma_done);  // every MMA is done before tensor memory is freed
             const volatile int never = 0;
