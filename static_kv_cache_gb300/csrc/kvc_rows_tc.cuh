@@ -563,30 +563,26 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             if (!ok) give_up();
         } else if (warp == C::MMA_WARP) {
             // ------------------------------------------------------------ MMAs
-            // The whole warp walks the loop, one elected lane issues: the operands'
-            // descriptors then stay warp-uniform, and each is its tile's plus a constant.
-            // The warp is brought together behind every wait and every issue: the
-            // instructions take their operands from registers that the warp's lanes
-            // share, and lanes that ran ahead of the issuing one would overwrite them
-            // (a commit then went to an address of nobody's).
-            // Tiles are taken in ring order, ahead of the wait for P: what stands
-            // between that wait and the MMAs is idle time of the tensor cores.
-            const bool leader = rows_elect();
-            constexpr uint32_t HI1 = rows_desc_hi(1024), HI2 = rows_desc_hi(2048);
-            bool ok = true;
-            RowsItem it;
-            uint32_t stage = 0, phase = 0;                                   // next tile of the ring
-            uint32_t tiles_a = 0, tiles_b = 0, items_a = 0, items_b = 0;     // of each stream
-            auto wait = [&](uint32_t bar, uint32_t parity) { ok = __all_sync(FULL, ok && rows_wait(bar, parity, flags, a.timeout_ns)); };
-            auto take_tile = [&]() {
-                wait(full + 8 * stage, phase);
-                const uint32_t s = stage;
-                if (++stage == NS) stage = 0, phase ^= 1;
-                return s;
-            };
-            auto issue_s = [&](int x, int qx, uint32_t s, bool paged) {
-                const uint32_t kt = (ring + s * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
-                if (leader) {
+            // One thread waits and issues.  Tiles are taken in ring order, ahead of
+            // the wait for P: what stands between that wait and the MMAs is idle time
+            // of the tensor cores.  (A whole warp with one elected lane issuing has
+            // to be brought together behind every wait and issue -- operands are in
+            // registers that the warp shares -- and measured 2 % slower.)
+            if (rows_elect()) {
+                constexpr uint32_t HI1 = rows_desc_hi(1024), HI2 = rows_desc_hi(2048);
+                bool ok = true;
+                RowsItem it;
+                uint32_t stage = 0, phase = 0;                                   // next tile of the ring
+                uint32_t tiles_a = 0, tiles_b = 0, items_a = 0, items_b = 0;     // of each stream
+                auto wait = [&](uint32_t bar, uint32_t parity) { ok = ok && rows_wait(bar, parity, flags, a.timeout_ns); };
+                auto take_tile = [&]() {
+                    wait(full + 8 * stage, phase);
+                    const uint32_t s = stage;
+                    if (++stage == NS) stage = 0, phase ^= 1;
+                    return s;
+                };
+                auto issue_s = [&](int x, int qx, uint32_t s, bool paged) {
+                    const uint32_t kt = (ring + s * C::TILE_BYTES) >> 4, qt = (sb + qx * C::TILE_BYTES) >> 4, s_t = tmem + C::S_COL + 128 * x;
                     if (CB == 2 && paged) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
@@ -599,12 +595,9 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                                            rows_desc(kt + (((ks >> 2) * BLK + (ks & 3) * 32) >> 4), HI1), IDESC_S, ks > 0);
                     }
                     tc::commit(s_full + 8 * x);
-                }
-                __syncwarp();
-            };
-            auto issue_pv = [&](int x, uint32_t s, bool paged, bool first) {
-                const uint32_t vt = (ring + s * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
-                if (leader) {
+                };
+                auto issue_pv = [&](int x, uint32_t s, bool paged, bool first) {
+                    const uint32_t vt = (ring + s * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
                     if (CB == 2 && paged) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
@@ -615,72 +608,69 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         for (int ks = 0; ks < 8; ++ks)
                             tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 2048) >> 4) + ((BLK >> 4) << 16), HI1), IDESC_O, ks > 0 || !first);
                     }
-                }
-                __syncwarp();
-            };
-            auto commit_to = [&](uint32_t bar) {
-                if (leader) tc::commit(bar);
-                __syncwarp();
-            };
-            for (int k = 0; ok; ++k) {
-                ok = __all_sync(FULL, take_item(k, it));
-                __syncwarp();
-                if (!ok) break;
-                if (lane == 0) dev::mbar_arrive(item_empty + 8 * (k & 1));
-                if (it.b < 0) break;
-                const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
-                const bool fold = nx == 1 && n > 1;
-                const int cached = a.block_table ? it.np - it.j0 : 0;  // the item's tiles j < cached are pages
-                wait(q_full, uint32_t(k) & 1);
-                uint32_t sk = take_tile(), sv = 0;
-                if (!ok) break;
-                tc::fence_after();
-                issue_s(0, 0, sk, 0 < cached);
-                if (fold) {
-                    commit_to(empty + 8 * sk);
-                    sk = take_tile();
+                };
+                for (int k = 0; ok; ++k) {
+                    ok = take_item(k, it);
+                    if (!ok) break;
+                    dev::mbar_arrive(item_empty + 8 * (k & 1));
+                    if (it.b < 0) break;
+                    const int n = it.j1 - it.j0, nx = it.ntok > TB ? 2 : 1;
+                    const bool fold = nx == 1 && n > 1;
+                    const int cached = a.block_table ? it.np - it.j0 : 0;  // the item's tiles j < cached are pages
+                    wait(q_full, uint32_t(k) & 1);
+                    uint32_t sk = take_tile(), sv = 0;
                     if (!ok) break;
                     tc::fence_after();
-                    issue_s(1, 0, sk, 1 < cached);
-                } else if (nx == 2) {
-                    issue_s(1, 1, sk, 0 < cached);
-                }
-                commit_to(empty + 8 * sk);
-                if (n == (fold ? 2 : 1)) commit_to(q_empty);
-                const int steps = fold ? n : n * nx;
-                for (int u = 0; u < steps; ++u) {
-                    const int x = fold || nx == 2 ? u & 1 : 0, j = fold || nx == 1 ? u : u >> 1;
-                    const int jn = fold ? j + 2 : j + 1;  // the stream's next tile
-                    const bool first = fold ? j < 2 : j == 0, take = fold || x == 0, release = fold || x == nx - 1;
-                    if (take) {
-                        sv = take_tile();
-                        if (jn < n) sk = take_tile();
+                    issue_s(0, 0, sk, 0 < cached);
+                    if (fold) {
+                        tc::commit(empty + 8 * sk);
+                        sk = take_tile();
+                        if (!ok) break;
+                        tc::fence_after();
+                        issue_s(1, 0, sk, 1 < cached);
+                    } else if (nx == 2) {
+                        issue_s(1, 1, sk, 0 < cached);
                     }
-                    const uint32_t items = x ? items_b : items_a;
-                    if (first && items > 0) wait(o_free + 8 * x, (items - 1) & 1);
-                    wait(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1);
-                    if (!ok) break;
-                    ++(x ? tiles_b : tiles_a);
-                    tc::fence_after();
-                    issue_pv(x, sv, j < cached, first);
-                    if (jn < n) {
-                        if (release) commit_to(empty + 8 * sv);
-                        issue_s(x, fold ? 0 : x, sk, jn < cached);
-                        if (release) {
-                            commit_to(empty + 8 * sk);
-                            if (jn == n - 1) commit_to(q_empty);
+                    tc::commit(empty + 8 * sk);
+                    if (n == (fold ? 2 : 1)) tc::commit(q_empty);
+                    const int steps = fold ? n : n * nx;
+                    for (int u = 0; u < steps; ++u) {
+                        const int x = fold || nx == 2 ? u & 1 : 0, j = fold || nx == 1 ? u : u >> 1;
+                        const int jn = fold ? j + 2 : j + 1;  // the stream's next tile
+                        const bool first = fold ? j < 2 : j == 0, take = fold || x == 0, release = fold || x == nx - 1;
+                        if (take) {
+                            sv = take_tile();
+                            if (jn < n) sk = take_tile();
                         }
-                    } else {
-                        commit_to(o_full + 8 * x);
-                        if (release) commit_to(empty + 8 * sv);
-                        ++(x ? items_b : items_a);
+                        const uint32_t items = x ? items_b : items_a;
+                        if (first && items > 0) wait(o_free + 8 * x, (items - 1) & 1);
+                        wait(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1);
+                        if (!ok) break;
+                        ++(x ? tiles_b : tiles_a);
+                        tc::fence_after();
+                        issue_pv(x, sv, j < cached, first);
+                        if (jn < n) {
+                            if (release) tc::commit(empty + 8 * sv);
+                            issue_s(x, fold ? 0 : x, sk, jn < cached);
+                            if (release) {
+                                tc::commit(empty + 8 * sk);
+                                if (jn == n - 1) tc::commit(q_empty);
+                            }
+                        } else {
+                            tc::commit(o_full + 8 * x);
+                            if (release) tc::commit(empty + 8 * sv);
+                            ++(x ? items_b : items_a);
+                        }
                     }
                 }
+                if (!ok) {
+                    if (!flags[0]) dev::record_error(a.err, ERR_TIMEOUT);
+                    flags[0] = 1;
+                }
+                tc::commit(mma_done);  // every MMA is done before tensor memory is freed
+                const volatile int never = 0;
+                rows_wait(mma_done, 0, &never, a.timeout_ns);
             }
-            if (!ok) give_up();
-            commit_to(mma_done);  // every MMA is done before tensor memory is freed
-            const volatile int never = 0;
-            rows_wait(mma_done, 0, &never, a.timeout_ns);
             __syncwarp();
         }
     } else {
