@@ -205,6 +205,60 @@ def test_rows_that_see_nothing_are_zero(dtype):
     check_tree(c, T, [0, 20, 0], [37, 37, 30], seen)
 
 
+@pytest.mark.parametrize("dtype,paged", [("bf16", False), ("fp16", True), ("fp32", False)])
+@pytest.mark.parametrize("T", [7, 70, 140])
+def test_infinities_and_nan_reach_the_tokens_that_see_them(dtype, paged, T):
+    """In V rows of drafted tokens; K rows of tokens that nobody sees hold NaN."""
+    c = _rows.Cache(dtype, 1, 2, 8, 2, 64, 320, paged=paged, seed=40 + T)
+    cached = [300, 0]
+    c.fill(0, cached)
+    seen = torch.stack([_rows.tree(T, T), _rows.tree(T, T + 1)])
+    dead = T - 2
+    seen[:, :, dead] = False
+    q, k, v = drafts(c, [T, T], None, T)
+    k[:, :, dead] = float("nan")
+    v[:, :, dead, 3] = float("inf")
+    v[0, 0, 1, 5], v[0, 1, T // 2, 0], v[1, 0, 2, 63], v[1, 0, 4, 63] = (float(x) for x in ("inf", "nan", "inf", "-inf"))
+    out = torch.zeros_like(q)
+    assert c.kvc.kvc_tree_attn(c.h, 0, q, k, v, _rows.ints(cached), None, _rows.words(seen), T, 0, c.scratch.data,
+                               c.scratch.nbytes, out, None) == 0
+    assert c.error() == 0
+    for b in range(2):
+        m = cached[b]
+        ref = rows.attend(q[b], c.at(c.K, 0, b, range(m)), c.at(c.V, 0, b, range(m)), k[b], v[b], seen[b])
+        assert not torch.isfinite(ref[0]).all()
+        _rows.close(out[b], *ref, dtype, 64, m + T)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_prompts_infinities_reach_later_tokens_only(dtype):
+    c = _rows.Cache(dtype, 1, 3, 4, 1, 128, 64, seed=50)
+    lens = [150, 30, 77]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = c.draw(257, 4, 128, tag="q"), c.draw(257, 1, 128, tag="k"), c.draw(257, 1, 128, tag="v")
+    v[140, 0, 7], v[150, 0, 0], v[256, 0, 1] = float("nan"), float("inf"), float("-inf")
+    out = torch.zeros_like(q)
+    assert c.kvc.kvc_prompt_attn(c.h, 0, q, k, v, _rows.ints(cu), None, 257, c.scratch.data, c.scratch.nbytes, out, None) == 0
+    assert c.error() == 0
+    empty = torch.zeros(1, 0, 128, device="cuda")
+    for b, n in enumerate(lens):
+        a = int(cu[b])
+        ref = rows.attend(q[a:a + n].transpose(0, 1), empty, empty, k[a:a + n].transpose(0, 1), v[a:a + n].transpose(0, 1),
+                          torch.ones(n, n, dtype=torch.bool).tril())
+        _rows.close(out[a:a + n].transpose(0, 1), *ref, dtype, 128, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_large_scores(dtype):
+    """Scores far apart: the reference maximum moves from tile to tile."""
+    c = _rows.Cache(dtype, 1, 1, 4, 2, 128, 700, seed=60)
+    c.fill(0, [700])
+    ramp = torch.linspace(0.2, 12, 700, device="cuda")[torch.randperm(700, generator=torch.Generator().manual_seed(1)).cuda()]
+    c.K[0, 0] *= ramp[:, None].to(c.tdt)
+    check_tree(c, 40, [700], None, torch.stack([_rows.tree(40, 3)]))
+    check_prompt(c, [200], [700])
+
+
 def test_bad_tree_arguments_are_skipped():
     c = _rows.Cache("bf16", 1, 4, 4, 2, 64, 64, seed=13)
     c.fill(0, [10, 64, 20, 5])
