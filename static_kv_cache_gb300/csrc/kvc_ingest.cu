@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constan
     __shared__ int warp_sum[8];
     __shared__ int found_s[4];  // sequence, first token of the chunk in it, tokens, cache position of that token
     __shared__ int64_t row_s[TOKENS], step_s[TOKENS];
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t chunk = blockIdx.x;; chunk += gridDim.x) {
         int64_t base = 0;  // chunks of the sequences before this batch
@@ -136,8 +136,8 @@ constexpr int STEPS = 8;
 
 template <bool INT8>
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ IngestArgs a) {
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int lane = threadIdx.x & 31, layer = blockIdx.y;
     const unsigned chunks = unsigned(a.P + STEPS - 1) / STEPS, segs = unsigned(a.B) * a.H_kv;
     const unsigned u = blockIdx.x * 8 + (threadIdx.x >> 5);  // (sequence, KV head, chunk)

@@ -48,8 +48,8 @@ __device__ __forceinline__ int entry(const PagesArgs &a, int x) {
 __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesArgs a, const int32_t *__restrict__ parent,
                                                    int cols) {
     extern __shared__ int32_t old[];  // [B][cols]
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int c0 = blockIdx.x * cols, nc = min(cols, a.max_blocks - c0);
     for (int x = threadIdx.x; x < a.B * nc; x += blockDim.x) {
         const int b = x / nc, j = x - b * nc;
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
 
 // ---- free ------------------------------------------------------------------
 __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ PagesArgs a, const int32_t *__restrict__ keep) {
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int64_t total = int64_t(a.B) * a.max_blocks;
     for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < total; x += int64_t(gridDim.x) * blockDim.x) {
         const int b = int(x / a.max_blocks), j = int(x - int64_t(b) * a.max_blocks);
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ P
     int32_t *first = dyn, *offset = dyn + a.B;  // [B] first logical block, [B + 1] first place
     __shared__ int part[32];
     __shared__ int copies;
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int tid = threadIdx.x;
     int4 count4 = make_int4(1, 1, 1, 1);  // the first 4096 counts: on their way meanwhile
     if (4 * tid + 3 < a.num_blocks) count4 = *reinterpret_cast<const int4 *>(a.refs + 4 * tid);
@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ P
 // them the pages that move.
 __global__ void __launch_bounds__(1024) compact_plan_kernel(const __grid_constant__ PagesArgs a, int32_t *n_live) {
     __shared__ int part[32];
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int tid = threadIdx.x;
     int n = 0;
     for (int x = tid; x < a.num_blocks; x += 1024) n += a.refs[x] > 0;
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(1024) compact_plan_kernel(const __grid_constan
 // table entry through `where`.
 template <bool REMAP>
 __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ PagesArgs a, int n_pairs) {
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     if constexpr (REMAP) {
         const int64_t total = int64_t(a.B) * a.max_blocks;
         for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < total; x += int64_t(gridDim.x) * blockDim.x) {

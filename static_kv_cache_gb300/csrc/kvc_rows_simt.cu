@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
     __shared__ __align__(16) uint4 ks[KEYS * (CH + 1)];
     __shared__ __align__(16) T vs[KEYS * D];
     __shared__ __align__(16) float qs[ROWS * D];
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // `parts` blocks share the rows of a segment

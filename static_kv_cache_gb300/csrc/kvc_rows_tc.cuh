@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
 
     auto give_up = [&]() {
         if (lane == 0) {
@@ -903,25 +903,24 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     if (fold) dev::mbar_arrive(o_free);
                 }
             };
-            if (it.slot < 0 && !any_odd) {
+            if (it.slot < 0 && !any_odd && !fold) {
                 // the whole item, as fragments of 16 query rows x D columns: four
                 // lanes hold 32 columns of a row and, transposed, write 64
                 // contiguous bytes (a row per lane, 16 bytes at a time, would keep
                 // the store path busy four times as long).  A row of zeros where
                 // nothing was seen, whatever the accumulator holds
-                const float g_b = l > 0.f ? f_b * inv : 0.f, g_a = l > 0.f ? f_a * inv : 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t o[D / 32][16];
                     const uint32_t at = o_t + (uint32_t(16 * h) << 16);
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q) rows_tmem_ld_frag(at + 32 * q, o[q]);
-                    float gb[2], ga[2];
+                    float2 g[2];
                     T *to[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        gb[i] = __shfl_sync(FULL, g_b, 16 * h + 8 * i + (lane >> 2));
-                        ga[i] = __shfl_sync(FULL, g_a, 16 * h + 8 * i + (lane >> 2));
+                        const float gi2 = __shfl_sync(FULL, inv, 16 * h + 8 * i + (lane >> 2));
+                        g[i] = make_float2(gi2, gi2);
                         const int tok = qx * TB + frag_tok[2 * h + i];
                         to[i] = frag_tok[2 * h + i] < TB && tok < it.ntok
                                     ? reinterpret_cast<T *>(a.out) + rows_offset(a, sq, it.b, H, it.kv * G + frag_head[2 * h + i], it.t0 + tok, D) + 8 * (lane & 3)
@@ -930,21 +929,6 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q) rows_reg_fence16(o[q]);
-                    if (fold) {
-#pragma unroll
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t oa[16];
-                            rows_tmem_ld_frag(at - D + 32 * q, oa);
-                            tc::tmem_ld_wait();
-                            rows_reg_fence16(oa);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int i = (e >> 1) & 1;
-                                o[q][e] = __float_as_uint(fmaf(__uint_as_float(o[q][e]), gb[i], __uint_as_float(oa[e]) * ga[i]));
-                            }
-                        }
-                        gb[0] = gb[1] = 1.f;
-                    }
                     if (h == 1) release();
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q)
@@ -952,8 +936,10 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         for (int i = 0; i < 2; ++i) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int n4 = 0; n4 < 4; ++n4)
-                                w[n4] = Ops::pack(__uint_as_float(o[q][4 * n4 + 2 * i]) * gb[i], __uint_as_float(o[q][4 * n4 + 2 * i + 1]) * gb[i]);
+                            for (int n4 = 0; n4 < 4; ++n4) {
+                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[q][4 * n4 + 2 * i]), __uint_as_float(o[q][4 * n4 + 2 * i + 1])), g[i]);
+                                w[n4] = g[i].x > 0.f ? Ops::pack(y.x, y.y) : 0u;
+                            }
                             rows_quad_transpose(w, lane);
                             if (to[i]) *reinterpret_cast<uint4 *>(to[i] + 32 * q) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
@@ -962,7 +948,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 continue;
             }
             // a piece: its accumulator, four columns of the tile's rows after one
-            // another; or an item with infinities or NaN among its V rows
+            // another; or a whole item that is folded or has infinities or NaN among
+            // its V rows, a row per lane
             float *prow = nullptr;
             if (row_ok && it.slot >= 0) {
                 prow = a.part_acc + int64_t(it.slot) * 256 * D + 4 * (128 * qx + r);
@@ -1051,8 +1038,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
 // out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsTcArgs a) {
-    dev::grid_dependency_wait();
     dev::allow_dependents();
+    dev::grid_dependency_wait();
     const int i = blockIdx.x;
     const RowsCut cut = a.cuts[i];
     if (cut.pieces == 0) return;
