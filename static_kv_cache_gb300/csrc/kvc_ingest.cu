@@ -115,24 +115,36 @@ __global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constan
                               (is_v ? a.v_scale : a.k_scale) + row, lane);
             }
         } else {
-            const int per = a.H_kv * a.row_vecs;  // vectors of a token
-            for (int x = threadIdx.x; x < nt * per; x += blockDim.x) {
-                const int i = x / per, y = x - i * per, j = y / a.row_vecs, v = y - j * a.row_vecs;
-                if (row_s[i] < 0) continue;
-                const int64_t to = (row_s[i] + j * step_s[i]) * a.row_vecs + v, from = (int64_t(t0) + i) * per + y;
-                const uint4 kk = __ldg(reinterpret_cast<const uint4 *>(a.k_new) + from);
-                const uint4 vv = __ldg(reinterpret_cast<const uint4 *>(a.v_new) + from);
-                reinterpret_cast<uint4 *>(a.K)[to] = kk;
-                reinterpret_cast<uint4 *>(a.V)[to] = vv;
+            // four vectors of K and four of V in flight per thread
+            const int per = a.H_kv * a.row_vecs, all = nt * per;  // vectors of a token, of the chunk
+            const uint4 *ks = reinterpret_cast<const uint4 *>(a.k_new) + int64_t(t0) * per, *vs = reinterpret_cast<const uint4 *>(a.v_new) + int64_t(t0) * per;
+            for (int x0 = threadIdx.x; x0 < all; x0 += 4 * 256) {
+                uint4 k[4], v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = x0 + 256 * e;
+                    if (x < all) k[e] = __ldcs(ks + x), v[e] = __ldcs(vs + x);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = x0 + 256 * e, i = x / per, y = x - i * per, j = y / a.row_vecs;
+                    if (x >= all || row_s[i] < 0) continue;
+                    const int64_t to = (row_s[i] + j * step_s[i]) * a.row_vecs + y - j * a.row_vecs;
+                    reinterpret_cast<uint4 *>(a.K)[to] = k[e];
+                    reinterpret_cast<uint4 *>(a.V)[to] = v[e];
+                }
             }
         }
     }
 }
 
-// A warp takes eight path positions of one (layer, sequence, KV head), K and V:
-// one lane each looks up a position's source and destination, then every row
-// moves with four vectors of K and four of V in flight per lane.
-constexpr int STEPS = 8;
+// A warp takes 16 path positions of one (layer, sequence, KV head), K and V:
+// one lane each looks up a position's source and destination, then the rows
+// move with four vectors of K and four of V in flight per lane.  The path
+// entries of the check are the ones that are used, so that three dependent loads
+// (counts; path and table; rows) stand between the launch and the stores: at
+// 78 MB they, not the 12 us of the bytes, are most of the 20 us.
+constexpr int STEPS = 16;
 
 template <bool INT8>
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ IngestArgs a) {
@@ -145,10 +157,12 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
     const unsigned seg = u / chunks, chunk = u - seg * chunks, b = seg / a.H_kv, kv = seg - b * a.H_kv;
     const int n = __ldg(a.n_accept + b), c = __ldg(a.cache_index + b), i0 = int(chunk) * STEPS;
     bool bad = n < 0 || n > a.P || c < 0 || c > a.max_ctx || n > a.max_ctx - c;
+    int node = 0;  // path entry 32 (i0 / 32) + lane
     if (!bad && (i0 < n || chunk == 0)) {
         for (int i = lane; i < n; i += 32) {
             const int s = __ldg(a.path + int64_t(b) * a.P + i);
             bad = bad || s < 0 || s >= a.T;
+            if (i / 32 == i0 / 32) node = s;
         }
         bad = __any_sync(0xffffffffu, bad);
     }
@@ -159,9 +173,10 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
     const int steps = min(STEPS, n - i0);
     if (steps <= 0) return;
     int64_t to = -1, from = 0;  // lane i: row of position i0 + i in the cache and in k_new / v_new
+    node = __shfl_sync(0xffffffffu, node, (i0 & 31) + (lane & (STEPS - 1)));
     if (lane < steps) {
         int64_t row, step;
-        from = (int64_t(layer) * segs + seg) * a.T + __ldg(a.path + int64_t(b) * a.P + i0 + lane);
+        from = (int64_t(layer) * segs + seg) * a.T + node;
         if (cache_row(a, b, c + i0 + lane, row, step))
             to = row + kv * step;
         else

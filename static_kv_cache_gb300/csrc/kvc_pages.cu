@@ -329,13 +329,13 @@ __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ Pages
         const uint4 *from = pool + (int64_t(src) * a.H_kv + kv) * PAGE * a.row_vecs;
         uint4 *to = pool + (int64_t(dst) * a.H_kv + kv) * PAGE * a.row_vecs;
         const int vecs = rows * a.row_vecs;
-        for (int x = lane; x < vecs; x += 128) {  // four vectors in flight
-            uint4 v[4];
+        for (int x = lane; x < vecs; x += 256) {  // eight vectors in flight
+            uint4 v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (x + 32 * e < vecs) v[e] = from[x + 32 * e];
+            for (int e = 0; e < 8; ++e)
+                if (x + 32 * e < vecs) v[e] = __ldcs(from + x + 32 * e);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
                 if (x + 32 * e < vecs) to[x + 32 * e] = v[e];
         }
     }
