@@ -360,7 +360,7 @@ kvc_status kvc_prefill_attn(kvc_cache *h, int32_t layer, const void *q,
 
 /* Bytes of workspace for one kvc_prompt_attn or kvc_tree_attn call: the
  * partial results (max, sum, accumulator) of sequences split over several
- * CTAs.  0 if cfg is invalid. */
+ * CTAs, 43 MB at d_head 128.  0 if cfg is invalid. */
 uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
 
 /* Causal attention of whole prompts of different lengths, packed one behind
@@ -382,7 +382,8 @@ uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
  *                sequence whose range is reversed or leaves [0, total] is
  *                skipped (its output rows are left unwritten) and
  *                KVC_ERR_DEVICE_INDEX is recorded.  Packed rows outside every
- *                sequence are left unwritten.
+ *                sequence are left unwritten; rows that two ranges share (which
+ *                takes a reversed one) get either sequence's output.
  *   cache_index  device int32 [B]: cached rows of each sequence, or NULL: no
  *                sequence has any.  Outside [0, max_context]: skipped and
  *                recorded like a bad range.

@@ -100,8 +100,10 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     constexpr int SHORT = 8;
     a.min_share = 4;
     a.split_min = item > SHORT ? SHORT : 0x7fffffff;  // (nothing is cut where no combine follows)
+    // (no hint has a part in what fits the line)
+    const int64_t longest = (r.cache_index ? (c.max_context + 127) / 128 : 0) + (int64_t(max_tokens) + 127) / 128;
+    if (blocks * c.n_kv_heads * (longest + a.item_cost) > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     const int64_t line = blocks * c.n_kv_heads * (item + a.item_cost);
-    if (line > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     int64_t grid = h->num_sms < kvc::ROWS_MAX_CTAS ? h->num_sms : kvc::ROWS_MAX_CTAS;
     if ((line + a.min_share - 1) / a.min_share < grid) grid = (line + a.min_share - 1) / a.min_share;
     // the query tiles an item can fill
@@ -142,6 +144,8 @@ extern "C" {
 
 uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg) {
     if (kvc_workspace_bytes(cfg) == 0) return 0;
+    // (the kernel on the CUDA cores splits nothing)
+    if ((cfg->dtype != KVC_BF16 && cfg->dtype != KVC_FP16) || (cfg->d_head != 64 && cfg->d_head != 128)) return 256;
     uint64_t ml, acc;
     return kvc::rows_workspace(cfg->d_head, &ml, &acc);
 }

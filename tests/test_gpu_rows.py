@@ -383,3 +383,96 @@ def test_the_same_call_gives_the_same_bits():
                                    c.scratch.nbytes, out, None) == 0
         outs.append(out.view(torch.int16).clone())
     assert all(torch.equal(outs[0], x) for x in outs[1:])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_offsets_past_32_bits(paged):
+    """A layer of 5 GB per tensor: the last sequence's rows lie past 2^32 bytes,
+    the second layer's past 2^32 elements."""
+    G, D, T, L = 8, 128, 81920, 2
+    B = 30
+    c = _rows.Cache("bf16", L, B, 16, G, D, T, paged=paged, spare=0, seed=70)
+    assert c.K[0].numel() * 2 > 1 << 32 and c.K.numel() > 1 << 32
+    cached = [0] * (B - 2) + [300, 4000]
+    if paged:   # the last blocks of the pool, in descending order
+        c.table[B - 1] = torch.arange(c.blocks - 1, c.blocks - 1 - T // 16, -1, device="cuda", dtype=torch.int32)
+        c.table[B - 2] = torch.arange(T // 16, device="cuda", dtype=torch.int32)
+    c.fill(1, cached)
+    nodes = [0] * (B - 2) + [5, 20]
+    seen = torch.stack([_rows.tree(20, s) for s in range(B)])
+    check_tree(c, 20, cached, nodes, seen, layer=1)
+    lens = [0] * (B - 2) + [40, 70]
+    check_prompt(c, lens, cached, layer=1)
+    # rows stored there by both calls
+    k, v = c.draw(70, G, D, tag="ak"), c.draw(70, G, D, tag="av")
+    cu = [0] * B + [70]
+    assert c.kvc.kvc_append_packed(c.h, 1, k, v, _rows.ints(cu), _rows.ints([0] * (B - 1) + [T - 70]), 70, None) == 0
+    kt, vt = c.draw(1, B, G, 9, D, tag="ck"), c.draw(1, B, G, 9, D, tag="cv")
+    path, n = np.tile(np.arange(4) * 2, (B, 1)), [0] * (B - 1) + [4]
+    assert c.kvc.kvc_tree_commit(c.h, 1, 1, kt, vt, _rows.ints([0] * (B - 1) + [T - 90]), _rows.ints(path), _rows.ints(n), 9, 4, None) == 0
+    assert c.error() == 0
+    assert torch.equal(c.at(c.K, 1, B - 1, range(T - 70, T)), k.transpose(0, 1)) and torch.equal(c.at(c.V, 1, B - 1, range(T - 70, T)), v.transpose(0, 1))
+    assert torch.equal(c.at(c.K, 1, B - 1, range(T - 90, T - 86)), kt[0, B - 1][:, ::2][:, :4])
+    assert torch.equal(c.at(c.V, 1, B - 1, range(T - 90, T - 86)), vt[0, B - 1][:, ::2][:, :4])
+    assert c.intact()
+
+
+def test_a_prompt_then_drafts_then_decoding():
+    """The calls as a server makes them, over pages: prompts of different
+    lengths attended and stored, a tree verified, its accepted path stored, a
+    decode step -- every output is the dense attention of the history so far."""
+    import oracle
+    from tests.test_gpu_pages import Pool
+    p = Pool(L=1, B=4, G=2, D=128, per=12, blocks=60, H=8)
+    k = p.kvc
+    ws = torch.empty(k.kvc_rows_workspace_bytes(p.cfg), dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    draw = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    hist = [torch.zeros(2, 2, 0, 128, device="cuda", dtype=torch.bfloat16) for _ in range(4)]   # [K or V, head, row, D]
+    length = [0] * 4
+    for lens in ([37, 1, 100, 0], [5, 60, 0, 3]):      # the second prompts continue the first ones
+        total = sum(lens)
+        cu = np.concatenate([[0], np.cumsum(lens)])
+        q, kk, vv = draw(total, 8, 128), draw(total, 2, 128), draw(total, 2, 128)
+        grown = [a + b for a, b in zip(length, lens)]
+        p.reserve(length, grown)
+        out = torch.zeros_like(q)
+        assert k.kvc_prompt_attn(p.h, 0, q, kk, vv, _rows.ints(cu), _rows.ints(length), total, ws, ws.numel(), out, None) == 0
+        assert k.kvc_append_packed(p.h, 0, kk, vv, _rows.ints(cu), _rows.ints(length), total, None) == 0
+        for b, n in enumerate(lens):
+            new = torch.stack([kk, vv])[:, cu[b]:cu[b + 1]].transpose(1, 2)
+            if n:
+                ref = rows.attend(q[cu[b]:cu[b + 1]].transpose(0, 1), hist[b][0], hist[b][1], new[0], new[1], torch.ones(n, n, dtype=torch.bool).tril())
+                _rows.close(out[cu[b]:cu[b + 1]].transpose(0, 1), *ref, "bf16", 128, grown[b])
+            hist[b] = torch.cat([hist[b], new], 2)
+        length = grown
+    for step in range(3):
+        T = 11
+        seen = torch.stack([_rows.tree(T, 10 * step + b) for b in range(4)])
+        q, kk, vv = draw(4, 8, T, 128), draw(4, 2, T, 128), draw(4, 2, T, 128)
+        out = torch.zeros_like(q)
+        assert k.kvc_tree_attn(p.h, 0, q, kk, vv, _rows.ints(length), None, _rows.words(seen), T, max(length), ws, ws.numel(), out, None) == 0
+        for b in range(4):
+            _rows.close(out[b], *rows.attend(q[b], hist[b][0], hist[b][1], kk[b], vv[b], seen[b]), "bf16", 128, length[b] + T)
+        last = [4 + b + step for b in range(4)]           # the accepted leaf of each tree, and its path
+        paths = [seen[b, last[b]].nonzero()[:, 0].tolist() for b in range(4)]
+        grown = [n + len(x) for n, x in zip(length, paths)]
+        p.reserve(length, grown)
+        path = np.zeros((4, T), int)
+        for b, x in enumerate(paths):
+            path[b, :len(x)] = x
+        assert k.kvc_tree_commit(p.h, 0, 1, kk, vv, _rows.ints(length), _rows.ints(path), _rows.ints([len(x) for x in paths]), T, T, None) == 0
+        for b, x in enumerate(paths):
+            hist[b] = torch.cat([hist[b], torch.stack([kk[b], vv[b]])[:, :, x]], 2)
+        length = grown
+        q1, k1, v1 = draw(4, 8, 128), draw(4, 2, 1, 128), draw(4, 2, 1, 128)
+        p.reserve(length, [n + 1 for n in length])
+        length = [n + 1 for n in length]
+        out = torch.zeros_like(q1)
+        assert k.kvc_decode_step(p.h, 0, q1, k1, v1, _rows.ints(length), max(length), out, None) == 0
+        for b in range(4):
+            hist[b] = torch.cat([hist[b], torch.stack([k1[b], v1[b]])], 2)
+            want = oracle.decode_attn(synth.to_bits(q1[b:b + 1]), synth.to_bits(hist[b][0][None].contiguous()),
+                                      synth.to_bits(hist[b][1][None].contiguous()), np.array([length[b]], np.int32), "bf16")
+            assert np.abs(out[b].float().cpu().numpy() - want[0]).max() <= 2e-2
+    assert k.kvc_get_error(p.h, None) == 0
