@@ -34,8 +34,8 @@
 // unnormalised accumulator and (max, sum) per piece in the workspace, and
 // rows_combine_kernel folds the pieces.
 //
-// Warps: 0-3 softmax and epilogue of stream A, 4-7 of stream B; 8 copies K and V
-// (one ring, in the order in which the MMAs take them); 9 issues the MMAs and
+// Warps: 0-3 softmax and epilogue of stream A, 4-7 of stream B; 8 copies K and 11
+// V (one ring, in the order in which the MMAs take them); 9 issues the MMAs and
 // owns tensor memory; 10 walks the items, hands them to the others and copies
 // their query rows.  Cached rows of a contiguous cache and new rows come as
 // boxes of 128 rows x 64 columns.  A page of 16 rows (of one KV head) comes as one
@@ -81,14 +81,15 @@ struct RowsTcCfg {
     static constexpr int ITEM_OFF = BAR_OFF + 8 * NBAR + 8 + 24;  // after the TMEM address and the flags
     static constexpr int FOLD_OFF = ITEM_OFF + 2 * 64;            // folded items: stream A's (max, sum) of each row
     static constexpr int SMEM = 1024 + FOLD_OFF + 128 * 8;
-    static constexpr int K_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10;
-    static constexpr int THREADS = 12 * 32;  // (the last warp only fills its warpgroup)
+    static constexpr int K_WARP = 8, MMA_WARP = 9, ITEM_WARP = 10, V_WARP = 11;
+    static constexpr int THREADS = 12 * 32;
     // registers: 168 a thread at launch; the softmax warpgroups take from the third
     static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
     static_assert(2 * REGS_SOFTMAX + REGS_OTHER == 3 * 168, "the launch's registers");
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // S_A, S_B (128 columns each), O_A, O_B (D each)
     static constexpr float RESCALE_LOG2 = 8.f;
+    static_assert(NS >= 5, "the copy warps' waits (below)");
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 
     // 16-byte chunk c of row r of a tile of 128 consecutive rows
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             dev::mbar_init(o_full + 8 * x, 1);       // the item's last PV_x is done
             dev::mbar_init(o_free + 8 * x, 4);       // its accumulator is read (folded items: by stream B's warps)
             dev::mbar_init(item_full + 8 * x, 1);
-            dev::mbar_init(item_empty + 8 * x, 10);  // every other warp has read the item
+            dev::mbar_init(item_empty + 8 * x, 11);  // every other warp has read the item
         }
         dev::mbar_init(q_full, 1);
         dev::mbar_init(q_empty, 1);   // the item's last S has read Q
@@ -421,7 +422,8 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         it = *reinterpret_cast<const RowsItem *>(smem + C::ITEM_OFF + 64 * (k & 1));
         return true;
     };
-    int issued = 0, queries = 0;  // stages filled by the copy warp, items whose queries were copied
+    uint32_t filled = 0, filled_phase = 0;  // copy warps: stages filled, and the phase of each last filling
+    int queries = 0;                        // items whose queries were copied
     if (warp >= C::K_WARP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
         if (warp == C::ITEM_WARP) {
@@ -489,12 +491,19 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 for (int i = lane; i < a.B; i += 32)
                     if (rows_seq(a, i).bad) dev::record_error(a.err, ERR_DEVICE_INDEX);
             if (!ok) give_up();
-        } else if (warp == C::K_WARP) {
+        } else if (warp == C::K_WARP || warp == C::V_WARP) {
             // ------------------------------------------------------------ K and V copies
+            // One warp each: sixteen boxes of pages a tile pair from one warp were too
+            // slow (tree steps of 16 users on pages 71 -> 67 us).  The waits: stages
+            // are let go in ring order and a warp's places are at most three apart, so
+            // when it waits for place p - NS, place p - 2 NS is known to be free.
+            const bool v = warp == C::V_WARP;
             // cached rows that one item reads leave L2 to what is read again
             const uint64_t pol = a.read_once ? dev::l2_evict_first_policy() : dev::l2_evict_normal_policy();
+            const CUtensorMap *m_cache = v ? &a.tm_v : &a.tm_k, *m_new = v ? &a.tm_v_new : &a.tm_k_new;
             bool ok = true;
             RowsItem it;
+            uint32_t base = 0;  // ring places of the items before
             for (int k = 0; ok; ++k) {
                 ok = __all_sync(FULL, take_item(k, it));
                 __syncwarp();
@@ -503,65 +512,60 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 if (it.b < 0) break;
                 const int n = it.j1 - it.j0;
                 const bool fold = it.ntok <= TB && n > 1;
-                // the tile at place i, and whether it is V
-                auto tile_at = [&](int i) { return it.j0 + (fold ? (i == 2 * n - 1 ? n - 1 : i & 1 ? (i + 1) >> 1 : i ? (i >> 1) - 1 : 0) : i >> 1); };
                 // a page's number is looked up a tile ahead
-                auto page_at = [&](int i) {
-                    if (!a.block_table || lane >= 8 || i >= 2 * n) return 0;
-                    const int j = tile_at(i), blk = 8 * j + lane;
-                    return j < it.np && blk * 16 < it.c ? __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk) : 0;
+                auto page_of = [&](int jt) {
+                    const int blk = 8 * jt + lane;
+                    if (!a.block_table || lane >= 8 || jt >= it.np || blk * 16 >= it.c) return 0;
+                    return __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk);
                 };
-                int next_page = page_at(0);
-                for (int i = 0; i < 2 * n; ++i) {
-                    const int page = next_page, j = tile_at(i);
-                    const bool v = fold ? i > 0 && (i == 2 * n - 1 || !(i & 1)) : i & 1;
-                    next_page = page_at(i + 1);
-                    {
-                        const int s = issued % NS;
-                        if (issued >= NS)
-                            ok = __all_sync(FULL, rows_wait(empty + 8 * s, uint32_t(issued / NS - 1) & 1, flags, a.timeout_ns));
-                        if (!ok) break;
-                        const uint32_t dst = ring + uint32_t(s) * C::TILE_BYTES, bar = full + 8 * s;
-                        if (j >= it.np) {  // new rows
-                            const int jn = j - it.np;
-                            if (lane == 0) {
-                                dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-                                const CUtensorMap *m = v ? &a.tm_v_new : &a.tm_k_new;
+                int next_page = page_of(it.j0);
+                for (int j = 0; j < n; ++j) {
+                    const int page = next_page, jt = it.j0 + j;
+                    next_page = page_of(jt + 1);
+                    const uint32_t place = base + (v ? rows_v_place(fold, j, n) : rows_k_place(fold, j));
+                    const uint32_t s = place % NS, gen = place / NS;
+                    if (gen > 0) ok = __all_sync(FULL, rows_wait(empty + 8 * s, (gen - 1) & 1, flags, a.timeout_ns));
+                    if (!ok) break;
+                    filled |= 1u << s;
+                    filled_phase = (filled_phase & ~(1u << s)) | ((gen & 1) << s);
+                    const uint32_t dst = ring + s * C::TILE_BYTES, bar = full + 8 * s;
+                    if (jt >= it.np) {  // new rows
+                        const int row = 128 * (jt - it.np);
+                        if (lane == 0) {
+                            dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
 #pragma unroll
-                                for (int cb = 0; cb < CB; ++cb)
-                                    if (a.cu_seqlens)
-                                        dev::tma_load_3d(dst + cb * BLK, m, cb * 64, it.kv, it.row0 + 128 * jn, bar);
-                                    else
-                                        dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * jn, it.b * a.H_kv + it.kv, bar);
-                            }
-                        } else if (!a.block_table) {
-                            if (lane == 0) {
-                                dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-                                const CUtensorMap *m = v ? &a.tm_v : &a.tm_k;
-#pragma unroll
-                                for (int cb = 0; cb < CB; ++cb)
-                                    dev::tma_load_3d(dst + cb * BLK, m, cb * 64, 128 * j, a.seg_base + it.b * a.H_kv + it.kv, bar, pol);
-                            }
-                        } else {
-                            // the pages that hold cached rows, one lane each; a page out of
-                            // range is recorded and read as zeros (behind the pool's end)
-                            const int pages = min(8, (it.c - 128 * j + 15) / 16);
-                            if (lane == 0) dev::mbar_arrive_expect_tx(bar, uint32_t(pages) * CB * 2048);
-                            __syncwarp();
-                            if (lane < pages) {
-                                const bool in = page >= 0 && page < a.num_blocks;
-                                if (!in) dev::record_error(a.err, ERR_DEVICE_INDEX);
-                                dev::tma_load_5d(dst + lane * (CB * 2048), v ? &a.tm_v : &a.tm_k, 0, 0, 0, 0,
-                                                 in ? a.seg_base + page * a.H_kv + it.kv : a.pool_end, bar, pol);
-                            }
+                            for (int cb = 0; cb < CB; ++cb)
+                                if (a.cu_seqlens)
+                                    dev::tma_load_3d(dst + cb * BLK, m_new, cb * 64, it.kv, it.row0 + row, bar);
+                                else
+                                    dev::tma_load_3d(dst + cb * BLK, m_new, cb * 64, row, it.b * a.H_kv + it.kv, bar);
                         }
+                    } else if (!a.block_table) {
+                        if (lane == 0) {
+                            dev::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+#pragma unroll
+                            for (int cb = 0; cb < CB; ++cb)
+                                dev::tma_load_3d(dst + cb * BLK, m_cache, cb * 64, 128 * jt, a.seg_base + it.b * a.H_kv + it.kv, bar, pol);
+                        }
+                    } else {
+                        // the pages that hold cached rows, one lane each; a page out of
+                        // range is recorded and read as zeros (behind the pool's end)
+                        const int pages = min(8, (it.c - 128 * jt + 15) / 16);
+                        if (lane == 0) dev::mbar_arrive_expect_tx(bar, uint32_t(pages) * CB * 2048);
                         __syncwarp();
-                    ++issued;
+                        if (lane < pages) {
+                            const bool in = page >= 0 && page < a.num_blocks;
+                            if (!in) dev::record_error(a.err, ERR_DEVICE_INDEX);
+                            dev::tma_load_5d(dst + lane * (CB * 2048), m_cache, 0, 0, 0, 0,
+                                             in ? a.seg_base + page * a.H_kv + it.kv : a.pool_end, bar, pol);
+                        }
                     }
+                    __syncwarp();
                 }
+                base += 2 * n;
             }
             if (!ok) give_up();
-        } else if (warp == C::MMA_WARP) {
+        } else {
             // ------------------------------------------------------------ MMAs
             // One thread waits and issues.  Tiles are taken in ring order, ahead of
             // the wait for P: what stands between that wait and the MMAs is idle time
@@ -1025,10 +1029,10 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         const volatile int never = 0;
         rows_wait(q_full, uint32_t(queries - 1) & 1, &never, a.timeout_ns);
     }
-    if (warp == C::K_WARP && lane == 0 && flags[0]) {
+    if ((warp == C::K_WARP || warp == C::V_WARP) && lane == 0 && flags[0]) {
         const volatile int never = 0;
-        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-            rows_wait(full + 8 * (i % NS), uint32_t(i / NS) & 1, &never, a.timeout_ns);
+        for (int s = 0; s < NS; ++s)
+            if (filled >> s & 1) rows_wait(full + 8 * s, filled_phase >> s & 1, &never, a.timeout_ns);
     }
 }
 
