@@ -346,11 +346,8 @@ kvc_status kvc_prefill_attn(kvc_cache *h, int32_t layer, const void *q,
  * round-to-nearest-even at the end.  A 16-bit cache with d_head 64 or 128 runs
  * on the tensor cores, the others on the CUDA cores.
  *
- * Rows that a query does not see never reach its output, whatever finite
- * values they hold; cached rows at or past cache_index[b], and new rows past
- * the sequence's own, may hold anything.
- * (An infinity or NaN in a V row that one token of a sequence sees may reach
- * the other tokens of the same sequence and KV head.)
+ * Rows that a query does not see never reach its output, whatever they hold,
+ * infinities and NaN among it.
  *
  * The workspace of these calls (kvc_rows_workspace_bytes, 256-byte aligned)
  * need not be initialised and keeps nothing between calls; it may serve any
@@ -383,7 +380,8 @@ uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
  *                skipped (its output rows are left unwritten) and
  *                KVC_ERR_DEVICE_INDEX is recorded.  Packed rows outside every
  *                sequence are left unwritten; rows that two ranges share (which
- *                takes a reversed one) get either sequence's output.
+ *                takes a reversed one) get either sequence's output, or, where
+ *                the ranges together pass the limit below, none is written
  *   cache_index  device int32 [B]: cached rows of each sequence, or NULL: no
  *                sequence has any.  Outside [0, max_context]: skipped and
  *                recorded like a bad range.
@@ -393,7 +391,7 @@ uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
  * Paged handles: a block-table entry outside [0, num_blocks) among a
  * sequence's cached rows records KVC_ERR_DEVICE_INDEX; that sequence's output
  * is then undefined.  KVC_ERR_UNSUPPORTED also for a call whose product of
- * query blocks and key tiles passes 2^31 (over a million packed tokens).
+ * query blocks and key tiles passes 2000 * 2^20 (over a million packed tokens).
  * Host errors: KVC_ERR_INVALID, KVC_ERR_UNSUPPORTED, KVC_ERR_ALIGNMENT,
  * KVC_ERR_WORKSPACE, KVC_ERR_CUDA. */
 kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const void *k, const void *v,

@@ -73,6 +73,9 @@ struct RowsCut {
 
 // The tensor-core kernel's arguments (kvc_rows_tc.cuh).
 constexpr int ROWS_MAX_CTAS = 160;  // sizes the workspace
+// Length of the line of key tiles, at most.  (Places are 32-bit numbers; checked
+// in units of 2^20 rounded down per lane, hence the distance from 2^31.)
+constexpr int ROWS_MAX_LINE = 2000 << 20;
 struct RowsTcArgs : RowsArgs {
     RowsCut *cuts;               // [grid]
     float *part_ml;              // [2 grid][256][2]: (max, sum) of a piece's query rows

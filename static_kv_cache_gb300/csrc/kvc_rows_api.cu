@@ -102,7 +102,7 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     a.split_min = item > SHORT ? SHORT : 0x7fffffff;  // (nothing is cut where no combine follows)
     // (no hint has a part in what fits the line)
     const int64_t longest = (r.cache_index ? (c.max_context + 127) / 128 : 0) + (int64_t(max_tokens) + 127) / 128;
-    if (blocks * c.n_kv_heads * (longest + a.item_cost) > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
+    if (blocks * c.n_kv_heads * (longest + a.item_cost) > kvc::ROWS_MAX_LINE) return KVC_ERR_UNSUPPORTED;
     const int64_t line = blocks * c.n_kv_heads * (item + a.item_cost);
     int64_t grid = h->num_sms < kvc::ROWS_MAX_CTAS ? h->num_sms : kvc::ROWS_MAX_CTAS;
     if ((line + a.min_share - 1) / a.min_share < grid) grid = (line + a.min_share - 1) / a.min_share;

@@ -136,7 +136,8 @@ static_assert(sizeof(RowsItem) <= 64, "item slot");
 // Length on the line of the first q token blocks (of ti tokens) of one KV head
 // of a sequence: a.item_cost each for an item's start and end, and its key
 // tiles -- the cached ones, and of the new ones all under a mask, otherwise
-// those up to its last token.  (The host keeps the whole line below 2^31.)
+// those up to its last token.  (The host keeps the line of sequences that share
+// no rows below ROWS_MAX_LINE.)
 __device__ __forceinline__ int rows_prefix(const RowsTcArgs &a, const RowsSeq &s, int ti, int q) {
     const int base = q * (a.item_cost + (s.c + 127) / 128), kt = (s.n + 127) / 128;
     if (a.tree_mask) return base + q * kt;
@@ -189,9 +190,18 @@ struct RowsPlace {
 // odd lanes the next one's.
 __device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane, int &share, int &begin, int &end, RowsPlace &place) {
     constexpr unsigned FULL = 0xffffffffu;
-    int mine = 0, sum = 0;  // length of this lane's sequence (of the last batch of 32)
+    int mine = 0;  // length of this lane's sequence (of the last batch of 32)
+    int64_t sum = 0;
     for (int i = lane; i < a.B; i += 32) sum += mine = rows_seq_length(a, rows_seq(a, i), ti) * a.H_kv;
-    const int total = __reduce_add_sync(FULL, sum);
+    // Sequences that share packed rows (their ranges are not in order) can be longer
+    // together than the host's bound, ROWS_MAX_LINE: then no item is taken.
+    if (__reduce_add_sync(FULL, int(min(sum >> 20, int64_t(1) << 20))) > (ROWS_MAX_LINE >> 20)) {
+        if (blockIdx.x == 0 && lane == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
+        share = a.min_share;
+        begin = end = 0;
+        return;
+    }
+    const int total = __reduce_add_sync(FULL, int(sum));
     share = (total + int(gridDim.x) - 1) / int(gridDim.x);
     if (share < a.min_share) share = a.min_share;
     const int64_t at64 = int64_t(share) * (blockIdx.x + (lane & 1));

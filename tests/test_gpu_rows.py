@@ -318,6 +318,34 @@ def test_refusals():
     assert k.kvc_tree_attn(q8.h, 0, p, p, p, p, None, None, 4, 0, p, big, p) == k.KVC_ERR_UNSUPPORTED
 
 
+def test_sequences_that_share_rows():
+    """Ranges 0..n, n..0, 0..n, ...: the reversed ones are recorded; the others
+    have no cached rows here, so that each gives the same output."""
+    n = 300
+    c = _rows.Cache("bf16", 1, 6, 4, 2, 64, 64, seed=31)
+    q, k, v = c.draw(n, 4, 64, tag="q"), c.draw(n, 2, 64, tag="k"), c.draw(n, 2, 64, tag="v")
+    ob, out = _rows.guarded(torch.full_like(q, UNTOUCHED))
+    assert c.kvc.kvc_prompt_attn(c.h, 0, q, k, v, _rows.ints([0, n] * 3 + [0]), None, n, c.scratch.data, c.scratch.nbytes, out, None) == 0
+    assert c.error() == c.kvc.KVC_ERR_DEVICE_INDEX and c.error() == 0
+    ref = rows.attend(q.transpose(0, 1), k[:0].transpose(0, 1), v[:0].transpose(0, 1), k.transpose(0, 1), v.transpose(0, 1),
+                      torch.ones(n, n, dtype=torch.bool).tril())
+    _rows.close(out.transpose(0, 1), *ref, c.dtype, c.D, n)
+    assert ob.canaries_intact()
+
+
+def test_sequences_that_share_rows_past_the_limit():
+    """2048 sequences of 8192 query blocks with 256 key tiles on average pass 2^31
+    together, though none does alone: nothing is written."""
+    n, B = 65536, 4096
+    c = _rows.Cache("bf16", 1, B, 32, 1, 64, 16, seed=32)
+    q, k = torch.zeros(n, 32, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(n, 1, 64, device="cuda", dtype=torch.bfloat16)
+    out = torch.full_like(q, UNTOUCHED)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda").repeat(B // 2 + 1)[:B + 1].contiguous()
+    assert c.kvc.kvc_prompt_attn(c.h, 0, q, k, k, cu, None, n, c.scratch.data, c.scratch.nbytes, out, None) == 0
+    assert c.error() == c.kvc.KVC_ERR_DEVICE_INDEX and c.error() == 0
+    assert (out == UNTOUCHED).all() and c.intact()
+
+
 @pytest.mark.parametrize("what", ["prompt", "tree"])
 def test_captured_and_replayed_on_another_stream(what):
     """Two handles' calls in one graph, on a side stream, with one workspace in
