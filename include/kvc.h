@@ -347,7 +347,9 @@ kvc_status kvc_prefill_attn(kvc_cache *h, int32_t layer, const void *q,
  * on the tensor cores, the others on the CUDA cores.
  *
  * Rows that a query does not see never reach its output, whatever they hold,
- * infinities and NaN among it.
+ * infinities and NaN among it.  A query that sees a key with a NaN or +infinite
+ * score gets NaN; one that sees none but -infinite scores counts as seeing
+ * nothing (zeros).
  *
  * The workspace of these calls (kvc_rows_workspace_bytes, 256-byte aligned)
  * need not be initialised and keeps nothing between calls; it may serve any

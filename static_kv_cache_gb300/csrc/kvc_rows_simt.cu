@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 const float m_new = fmaxf(m[k], mx);
-                if (m_new == -INFINITY) continue;  // nothing seen so far (the whole warp agrees)
-                const float corr = exp2f(m[k] - m_new);
-                const float p = see ? exp2f(x - m_new) : 0.f;
+                const float ref = m_new == -INFINITY ? 0.f : m_new;  // (nothing seen so far, or only NaN, which stays)
+                const float corr = exp2f(m[k] - ref);
+                const float p = see ? exp2f(x - ref) : 0.f;
                 m[k] = m_new;
                 l[k] = l[k] * corr + p;
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
             float sum = l[k];
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;  // a row that sees nothing: zeros
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing: zeros
             if (tok[k] >= 0) {
                 const int i = int((r0 + warp * RW + k) / s.n);
                 T *o = reinterpret_cast<T *>(a.out) + rows_offset(a, s, b, H, kv * a.group + i, tok[k], D);

@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 m_run = M;
             }
             const bool any_odd = odd[k & 3] != 0;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN, of a key row that is seen, passes)
             RowsSeq sq;
             sq.row0 = it.row0;
             auto release = [&]() {  // the accumulators are read: the next item's PV may overwrite them
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
 #pragma unroll
                             for (int n4 = 0; n4 < 4; ++n4) {
                                 const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[q][4 * n4 + 2 * i]), __uint_as_float(o[q][4 * n4 + 2 * i + 1])), g[i]);
-                                w[n4] = g[i].x > 0.f ? Ops::pack(y.x, y.y) : 0u;
+                                w[n4] = g[i].x != 0.f ? Ops::pack(y.x, y.y) : 0u;
                             }
                             rows_quad_transpose(w, lane);
                             if (to[i]) *reinterpret_cast<uint4 *>(to[i] + 32 * q) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         uint32_t u[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            u[i] = l > 0.f ? Ops::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv) : 0u;
+                            u[i] = l != 0.f ? Ops::pack(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv) : 0u;
                         *reinterpret_cast<uint4 *>(orow + e) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
         const float2 y = __ldcg(ml + slot(p));
         const float4 u = __ldcg(reinterpret_cast<const float4 *>(acc + slot(p) * D));
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(acc + slot(p) * D + 1024));
-        if (y.x == -INFINITY) continue;  // the row sees nothing of this piece
+        if (y.y == 0.f) continue;  // the row sees nothing of this piece
         const float m = fmaxf(M, y.x), fo = M == -INFINITY ? 0.f : ex2_approx(M - m), f = ex2_approx(y.x - m);
         M = m;
         L = L * fo + y.y * f;
@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = fmaf(w[e], f, o[e] * fo);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     const RowsSeq s = rows_seq(a, cut.b);
     uint32_t w[4];
 #pragma unroll

@@ -248,6 +248,49 @@ def test_a_prompts_infinities_reach_later_tokens_only(dtype):
         _rows.close(out[a:a + n].transpose(0, 1), *ref, dtype, 128, n)
 
 
+@pytest.mark.parametrize("dtype,D,paged", [("bf16", 64, True), ("fp16", 128, False), ("fp32", 64, False)])
+@pytest.mark.parametrize("T", [7, 70, 140])
+def test_infinite_and_nan_scores_in_a_tree(dtype, D, paged, T):
+    """In K rows of drafted tokens (an infinite element's score is +inf or -inf by
+    the sign of q) and in a cached one, which every token sees."""
+    c = _rows.Cache(dtype, 1, 3, 8, 2, D, 320, paged=paged, seed=70 + T)
+    cached = [300, 0, 200]
+    c.fill(0, cached)
+    c.put(c.K, 0, 2, [130], torch.full((2, 1, D), float("nan"), dtype=c.tdt, device="cuda"))
+    seen = torch.stack([_rows.tree(T, T + i) for i in range(3)])
+    q, k, v = drafts(c, [T] * 3, None, T)
+    k[0, 0, 3, 5], k[0, 1, T // 2, 0], k[1, 0, 4, 63], k[1, 1, T - 2, 1] = (float(x) for x in ("inf", "nan", "nan", "nan"))
+    out = torch.zeros_like(q)
+    assert c.kvc.kvc_tree_attn(c.h, 0, q, k, v, _rows.ints(cached), None, _rows.words(seen), T, 0, c.scratch.data,
+                               c.scratch.nbytes, out, None) == 0
+    assert c.error() == 0
+    for b in range(3):
+        m = cached[b]
+        ref = rows.attend(q[b], c.at(c.K, 0, b, range(m)), c.at(c.V, 0, b, range(m)), k[b], v[b], seen[b])
+        assert ref[0].isnan().all() if b == 2 else ref[0].isnan().any() and not ref[0].isnan().all()
+        _rows.close(out[b], *ref, dtype, D, m + T)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("m", [0, 2048])
+def test_infinite_and_nan_scores_in_a_prompt(dtype, m):
+    """Without cached rows, and with so many that the keys are split: the tokens
+    from the bad key on are NaN, also where a piece holds nothing else."""
+    c = _rows.Cache(dtype, 1, 1, 4, 1, 128, 2048, seed=80)
+    c.fill(0, [m])
+    n = 300
+    q, k, v = c.draw(n, 4, 128, tag="q"), c.draw(n, 1, 128, tag="k"), c.draw(n, 1, 128, tag="v")
+    k[200] = float("nan")
+    k[250, 0, 3] = float("inf")
+    out = torch.zeros_like(q)
+    assert c.kvc.kvc_prompt_attn(c.h, 0, q, k, v, _rows.ints([0, n]), _rows.ints([m]), n, c.scratch.data, c.scratch.nbytes, out, None) == 0
+    assert c.error() == 0
+    ref = rows.attend(q.transpose(0, 1), c.at(c.K, 0, 0, range(m)), c.at(c.V, 0, 0, range(m)), k.transpose(0, 1), v.transpose(0, 1),
+                      torch.ones(n, n, dtype=torch.bool).tril())
+    assert ref[0][:, 200:].isnan().all() and torch.isfinite(ref[0][:, :200]).all()
+    _rows.close(out.transpose(0, 1), *ref, dtype, 128, m + n)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_large_scores(dtype):
     """Scores far apart: the reference maximum moves from tile to tile."""
