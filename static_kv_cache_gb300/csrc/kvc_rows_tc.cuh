@@ -1046,12 +1046,12 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     }
 }
 
-// Folds the pieces of the items that CTA boundaries cut.  Block (i, y): 32 query
+// Folds the pieces of the items that CTA boundaries cut.  Block (i, y): 64 query
 // rows x 64 columns of the item that CTA i started; a thread takes eight columns
 // of a row, consecutive threads consecutive rows, as the pieces are laid out:
 // out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M).
 template <typename T, int D>
-__global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant__ RowsTcArgs a) {
+__global__ void __launch_bounds__(512) rows_combine_kernel(const __grid_constant__ RowsTcArgs a) {
     dev::allow_dependents();
     dev::grid_dependency_wait();
     const int i = blockIdx.x;
@@ -1059,7 +1059,7 @@ __global__ void __launch_bounds__(256) rows_combine_kernel(const __grid_constant
     if (cut.pieces == 0) return;
     const int G = a.group, TB = 128 / G;
     const int yr = blockIdx.y / (D / 64), yc = blockIdx.y % (D / 64);
-    const int r = 32 * yr + (threadIdx.x & 31), col = 64 * yc + 8 * (threadIdx.x >> 5);
+    const int r = 64 * yr + (threadIdx.x & 63), col = 64 * yc + 8 * (threadIdx.x >> 6);
     const int x = r >> 7, rt = (r & 127) / G, head = (r & 127) - rt * G, tok = x * TB + rt;
     if (rt >= TB || tok >= cut.ntok) return;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + r;
@@ -1101,7 +1101,7 @@ template <typename T, int D>
 cudaError_t launch_rows_tc(const RowsTcArgs &a, int grid, int combine_rows, cudaStream_t s) {
     const cudaError_t e = launch_pdl(rows_tc_kernel<T, D>, dim3(grid), dim3(RowsTcCfg<D>::THREADS), RowsTcCfg<D>::SMEM, s, a);
     if (e != cudaSuccess || combine_rows == 0 || grid == 1) return e;
-    return launch_pdl(rows_combine_kernel<T, D>, dim3(grid, (combine_rows + 31) / 32 * (D / 64)), dim3(256), 0, s, a);
+    return launch_pdl(rows_combine_kernel<T, D>, dim3(grid, (combine_rows + 63) / 64 * (D / 64)), dim3(512), 0, s, a);
 }
 
 template <typename T, int D>
