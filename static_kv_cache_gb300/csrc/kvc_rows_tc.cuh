@@ -76,8 +76,8 @@ struct RowsTcCfg {
     static constexpr int RING_OFF = 2 * TILE_BYTES;
     static constexpr int BAR_OFF = RING_OFF + NS * TILE_BYTES;
     // full[NS], empty[NS], s_full[2], p_full[2], o_full[2], o_free[2], q_full,
-    // q_empty, item_full[2], item_empty[2], fold, mma_done
-    static constexpr int NBAR = 2 * NS + 16;
+    // q_empty, item_full[2], item_empty[2], fold, mma_done, p_half[2]
+    static constexpr int NBAR = 2 * NS + 18;
     static constexpr int ITEM_OFF = BAR_OFF + 8 * NBAR + 8 + 24;  // after the TMEM address and the flags
     static constexpr int FOLD_OFF = ITEM_OFF + 2 * 64;            // folded items: stream A's (max, sum) of each row
     static constexpr int SMEM = 1024 + FOLD_OFF + 128 * 8;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
     const uint32_t ring = sb + C::RING_OFF;
     const uint32_t full = sb + C::BAR_OFF, empty = full + 8 * NS, s_full = empty + 8 * NS, p_full = s_full + 16,
                    o_full = p_full + 16, o_free = o_full + 16, q_full = o_free + 16, q_empty = q_full + 8,
-                   item_full = q_empty + 8, item_empty = item_full + 16, fold_bar = item_empty + 16, mma_done = fold_bar + 8;
+                   item_full = q_empty + 8, item_empty = item_full + 16, fold_bar = item_empty + 16, mma_done = fold_bar + 8, p_half = mma_done + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::NBAR);
     volatile int *flags = reinterpret_cast<volatile int *>(smem + C::BAR_OFF + 8 * C::NBAR + 8);  // abort, then odd[4]
     volatile int *odd = flags + 1;  // item i met infinities or NaN: odd[i % 4]
@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
         for (int x = 0; x < 2; ++x) {
             dev::mbar_init(s_full + 8 * x, 1);       // S_x is in tensor memory, PV_x before it done
             dev::mbar_init(p_full + 8 * x, 4);       // the four softmax warps wrote P_x
+            dev::mbar_init(p_half + 8 * x, 4);       // its first 64 columns
             dev::mbar_init(o_full + 8 * x, 1);       // the item's last PV_x is done
             dev::mbar_init(o_free + 8 * x, 4);       // its accumulator is read (folded items: by stream B's warps)
             dev::mbar_init(item_full + 8 * x, 1);
@@ -610,16 +611,17 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                     }
                     tc::commit(s_full + 8 * x);
                 };
-                auto issue_pv = [&](int x, uint32_t s, bool paged, bool first) {
+                auto issue_pv = [&](int x, uint32_t s, bool paged, bool first, auto half) {  // 64 of the tile's keys
+                    constexpr int K0 = 4 * decltype(half)::value;
                     const uint32_t vt = (ring + s * C::TILE_BYTES) >> 4, p_t = tmem + C::S_COL + 128 * x, o_t = tmem + C::O_COL + D * x;
                     if (CB == 2 && paged) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
+                        for (int ks = K0; ks < K0 + 4; ++ks)
                             tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 4096) >> 4) + ((1024 >> 4) << 16), HI2),
                                            IDESC_O, ks > 0 || !first);
                     } else {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
+                        for (int ks = K0; ks < K0 + 4; ++ks)
                             tc::mma_f16_ts(o_t, p_t + 8 * ks, rows_desc(vt + ((ks * 2048) >> 4) + ((BLK >> 4) << 16), HI1), IDESC_O, ks > 0 || !first);
                     }
                 };
@@ -658,11 +660,15 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         }
                         const uint32_t items = x ? items_b : items_a;
                         if (first && items > 0) wait(o_free + 8 * x, (items - 1) & 1);
-                        wait(p_full + 8 * x, (x ? tiles_b : tiles_a) & 1);
+                        const uint32_t ph = (x ? tiles_b : tiles_a)++ & 1;
+                        wait(p_half + 8 * x, ph);
                         if (!ok) break;
-                        ++(x ? tiles_b : tiles_a);
                         tc::fence_after();
-                        issue_pv(x, sv, j < cached, first);
+                        issue_pv(x, sv, j < cached, first, std::integral_constant<int, 0>());
+                        wait(p_full + 8 * x, ph);
+                        if (!ok) break;
+                        tc::fence_after();
+                        issue_pv(x, sv, j < cached, first, std::integral_constant<int, 1>());
                         if (jn < n) {
                             if (release) tc::commit(empty + 8 * sv);
                             issue_s(x, fold ? 0 : x, sk, jn < cached);
@@ -768,7 +774,10 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 }
                 if (!warp_ok) {
                     __syncwarp();
-                    if (lane == 0) dev::mbar_arrive(p_full + 8 * x);
+                    if (lane == 0) {
+                        dev::mbar_arrive(p_half + 8 * x);
+                        dev::mbar_arrive(p_full + 8 * x);
+                    }
                     continue;
                 }
                 // the columns that this row does not see
@@ -863,6 +872,12 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         pk[e / 2] = Ops::pack(p0, p1);
                     }
                     rows_tmem_st16(s_t + 16 * q, pk);  // over scores that are in registers
+                    if (q == 1) {
+                        tc::tmem_st_wait();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) dev::mbar_arrive(p_half + 8 * x);
+                    }
                 }
                 l2 = __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
                 tc::tmem_st_wait();
