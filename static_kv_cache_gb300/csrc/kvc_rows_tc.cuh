@@ -855,16 +855,14 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 const float2 neg2 = make_float2(negm, negm);
                 float2 ps[4] = {l2, make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1])), scale2, neg2);
                         sr[q][e] = __float_as_uint(y.x);
                         sr[q][e + 1] = __float_as_uint(y.y);
                     }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float p0 = ex2_approx(__uint_as_float(sr[q][e])), p1 = ex2_approx(__uint_as_float(sr[q][e + 1]));
