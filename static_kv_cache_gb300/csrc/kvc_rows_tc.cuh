@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         pk[e / 2] = Ops::pack(p0, p1);
                     }
                     rows_tmem_st16(s_t + 16 * q, pk);  // over scores that are in registers
-                    if (q == 1) {
+                    if (q == 1) {  // P.V starts on these 64 keys (long prompt 1623 -> 1583 us)
                         tc::tmem_st_wait();
                         tc::fence_before();
                         __syncwarp();
