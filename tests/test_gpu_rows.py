@@ -361,6 +361,48 @@ def test_refusals():
     assert k.kvc_tree_attn(q8.h, 0, p, p, p, p, None, None, 4, 0, p, big, p) == k.KVC_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("paged", [False, True])
+def test_many_sequences(paged):
+    """More sequences than a warp has lanes, a third of them without tokens."""
+    c = _rows.Cache("bf16", 1, 75, 4, 2, 64, 160, paged=paged, seed=33)
+    rng = np.random.default_rng(33)
+    cached = [int(x) for x in rng.integers(0, 161, 75)]
+    lens = [int(x) if i % 3 else 0 for i, x in enumerate(rng.integers(1, 200, 75))]
+    c.fill(0, cached)
+    check_prompt(c, lens, cached)
+    T = 9
+    check_tree(c, T, cached, [min(n, T) for n in lens], torch.stack([_rows.tree(T, i) for i in range(75)]))
+
+
+def test_two_streams_at_once():
+    """Calls on one handle that overlap, each with its own workspace."""
+    c = _rows.Cache("bf16", 1, 2, 8, 2, 128, 1024, seed=34)
+    c.fill(0, [1000, 700])
+    ws = [c.scratch, _rows._gpu.Guarded(c.kvc.kvc_rows_workspace_bytes(c.cfg))]
+    lens, cu = [300, 150], _rows.ints([0, 300, 450])
+    m = _rows.ints([1000, 700])
+    q = [c.draw(450, 8, 128, tag=("q", i)) for i in range(2)]
+    k, v = c.draw(450, 2, 128, tag="k"), c.draw(450, 2, 128, tag="v")
+
+    def call(i, out, stream):
+        assert c.kvc.kvc_prompt_attn(c.h, 0, q[i], k, v, cu, m, 450, ws[i].data, ws[i].nbytes, out, stream) == 0
+
+    alone = [torch.zeros_like(x) for x in q]
+    for i in range(2):
+        call(i, alone[i], None)
+        torch.cuda.synchronize()
+    assert torch.isfinite(alone[0].float()).all() and (alone[0] != alone[1]).any()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros_like(x) for x in q] for _ in range(20)]
+    torch.cuda.synchronize()
+    for o in outs:
+        for i in range(2):
+            call(i, o[i], streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[i], alone[i]) for o in outs for i in range(2))
+    assert c.error() == 0 and c.intact() and ws[1].canaries_intact()
+
+
 def test_sequences_that_share_rows():
     """Ranges 0..n, n..0, 0..n, ...: the reversed ones are recorded; the others
     have no cached rows here, so that each gives the same output."""
