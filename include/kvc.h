@@ -436,7 +436,8 @@ kvc_status kvc_append_packed(kvc_cache *h, int32_t layer, const void *k, const v
  *                 of row t: t attends to s.  Any mask is allowed; a token that
  *                 sees no row at all gets zeros.  NULL: a chain (t attends to
  *                 s <= t)
- *   T             1 .. max_context
+ *   T             >= 1 (it may pass max_context: the drafted rows are no part of
+ *                 the cache)
  *   max_index_hint  host; 0, or an upper bound on cache_index used only to size
  *                 the launch
  *   workspace     device, ws_bytes >= kvc_rows_workspace_bytes(cfg)

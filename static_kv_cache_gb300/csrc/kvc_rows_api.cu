@@ -93,7 +93,7 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     const int ti = 2 * (128 / h->group);
     const int64_t item = (max_cached + 127) / 128 + (int64_t(max_tokens) + 127) / 128;
     const int64_t blocks = r.cu_seqlens ? r.total / ti + (c.batch < r.total ? c.batch : r.total)
-                                        : int64_t(c.batch) * ((r.T + ti - 1) / ti);
+                                        : int64_t(c.batch) * ((int64_t(r.T) + ti - 1) / ti);
     a.read_once = !r.cu_seqlens && r.T <= ti;
     a.item_cost = 2;
     // An item of up to 8 key tiles takes about as long as its pieces' combine.
@@ -189,8 +189,7 @@ kvc_status kvc_append_packed(kvc_cache *h, int32_t layer, const void *k, const v
 kvc_status kvc_tree_attn(kvc_cache *h, int32_t layer, const void *q, const void *k_new, const void *v_new,
                          const int32_t *cache_index, const int32_t *n_nodes, const uint32_t *tree_mask, int32_t T,
                          int32_t max_index_hint, void *workspace, uint64_t ws_bytes, void *out, void *stream) {
-    if (!h || layer < 0 || layer >= h->cfg.n_layers || T < 1 || T > h->cfg.max_context || max_index_hint < 0 ||
-        max_index_hint > h->cfg.max_context)
+    if (!h || layer < 0 || layer >= h->cfg.n_layers || T < 1 || max_index_hint < 0 || max_index_hint > h->cfg.max_context)
         return KVC_ERR_INVALID;
     if (h->cfg.dtype == KVC_INT8) return KVC_ERR_UNSUPPORTED;
     if (!q || !k_new || !v_new || !cache_index || !out || !device_current(h)) return KVC_ERR_INVALID;
@@ -206,7 +205,7 @@ kvc_status kvc_tree_attn(kvc_cache *h, int32_t layer, const void *q, const void 
     a.n_nodes = n_nodes;
     a.tree_mask = tree_mask;
     a.T = T;
-    a.mask_words = (T + 31) / 32;
+    a.mask_words = int((int64_t(T) + 31) / 32);
     return launch_rows(h, a, T, max_index_hint ? max_index_hint : h->cfg.max_context, layer, workspace, stream);
 }
 

@@ -176,6 +176,13 @@ def test_paged_trees(dtype, H, G, D):
     check_tree(c, T, [640, 15, 333], None, torch.stack([_rows.tree(T, s) for s in range(3)]))
 
 
+@pytest.mark.parametrize("dtype,D,paged", [("bf16", 128, True), ("fp16", 64, False), ("fp32", 64, False)])
+def test_more_drafts_than_the_cache_has_rows(dtype, D, paged):
+    c = _rows.Cache(dtype, 1, 2, 4, 2, D, 16, paged=paged, seed=35)
+    c.fill(0, [16, 5])
+    check_tree(c, 150, [16, 5], [150, 140], torch.stack([_rows.tree(150, i) for i in range(2)]))
+
+
 def test_a_chain_needs_no_mask():
     c = _rows.Cache("bf16", 1, 2, 4, 1, 128, 300, seed=9)
     c.fill(0, [300, 7])
@@ -347,7 +354,7 @@ def test_refusals():
     assert call(total=0) == 0
     call = lambda **kw: k.kvc_tree_attn(c.h, *[{**dict(layer=0, q=p, k=p, v=p, c=p, n=None, m=None, T=4, hint=0, ws=p, nb=big, out=p), **kw}[x]  # noqa: E731
                                                for x in ("layer", "q", "k", "v", "c", "n", "m", "T", "hint", "ws", "nb", "out")])
-    assert call(layer=2) == call(T=0) == call(T=65) == call(hint=-1) == call(hint=65) == call(c=None) == k.KVC_ERR_INVALID
+    assert call(layer=2) == call(T=0) == call(T=-1) == call(hint=-1) == call(hint=65) == call(c=None) == k.KVC_ERR_INVALID
     assert call(q=p + 8) == call(out=p + 2) == k.KVC_ERR_ALIGNMENT
     assert call(ws=None) == call(nb=0) == k.KVC_ERR_WORKSPACE
     assert k.kvc_append_packed(c.h, 2, p, p, p, p, 1) == k.kvc_append_packed(c.h, 0, p, p, None, p, 1) == k.KVC_ERR_INVALID
