@@ -745,9 +745,6 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
             float2 l2 = make_float2(0.f, 0.f);
             const int j_first = fold ? x : 0;
             for (int j = j_first; j < n; j += fold ? 2 : 1, ++gt) {
-                ok = __all_sync(FULL, rows_wait(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
-                if (!ok) break;
-                tc::fence_after();
                 // the V rows that a partly visible tile has to be rid of (below)
                 const int jt = it.j0 + j;
                 const bool is_new = jt >= it.np;
@@ -755,13 +752,11 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 const int nv = min(128, (is_new ? it.vis : it.c) - key0);  // the tile's own rows
                 // does every row of the item see the whole tile?
                 const bool partial = nv < 128 || (is_new && (a.tree_mask || key0 + 127 > it.t0));
-                if (partial && (x == 0 || fold)) {
-                    // V rows behind the tile's own are zeroed, infinities and NaN of
-                    // rows that not everybody sees set aside (with two query tiles
-                    // PV_B follows PV_A, which waits for these warps)
+                // V rows behind the tile's own are zeroed, infinities and NaN of rows that
+                // not everybody sees set aside
+                auto clean = [&]() {
                     const uint32_t sv = st + rows_v_place(fold, j, n);
-                    ok = __all_sync(FULL, rows_wait(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns));
-                    if (!ok) break;
+                    if (!__all_sync(FULL, rows_wait(full + 8 * (sv % NS), (sv / NS) & 1, flags, a.timeout_ns))) return false;
                     const uint32_t vt = ring + (sv % NS) * C::TILE_BYTES;
                     const bool paged = a.block_table && !is_new;
                     for (int i = is_new ? r : r + nv * C::CHUNKS; i < 128 * C::CHUNKS; i += 128) {
@@ -779,7 +774,20 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         }
                     }
                     dev::fence_proxy_async_smem();
-                }
+                    return true;
+                };
+                // With two query tiles stream A's warps do it for both (PV_B follows PV_A,
+                // which waits for them), while the tile's S is on its way: what the V
+                // tile's stage held before is known to have arrived, as a later place's
+                // has.  Not so ahead of an item's first S, nor in folded items, where the
+                // other stream's tiles lie between.
+                const bool to_clean = partial && (x == 0 || fold), early = j > j_first && !fold;
+                if (to_clean && early) ok = clean();
+                ok = ok && __all_sync(FULL, rows_wait(s_full + 8 * x, gt & 1, flags, a.timeout_ns));
+                if (!ok) break;
+                if (to_clean && !early) ok = clean();
+                if (!ok) break;
+                tc::fence_after();
                 if (!warp_ok) {
                     __syncwarp();
                     if (lane == 0) {
