@@ -95,11 +95,16 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     const int64_t blocks = r.cu_seqlens ? r.total / ti + (c.batch < r.total ? c.batch : r.total)
                                         : int64_t(c.batch) * ((int64_t(r.T) + ti - 1) / ti);
     a.read_once = !r.cu_seqlens && r.T <= ti;
-    a.item_cost = 2;
-    // An item of up to 8 key tiles takes about as long as its pieces' combine.
+    // An item's start and end take about as long as three key tiles.  (Prompts over
+    // prefixes at 2, 3, 4 tiles: 231, 226, 222 us; short prompts 24.4, 23.8, 24.6; tree
+    // steps on pages 67.4, 67.5, 68.2)
+    a.item_cost = 3;
+    // Where no item passes 8 key tiles none is cut: it would take about as long as its
+    // pieces' combine.  Otherwise those past 4 are (past 8: prompts over prefixes 230
+    // instead of 226 us).
     constexpr int SHORT = 8;
     a.min_share = 4;
-    a.split_min = item > SHORT ? SHORT : 0x7fffffff;  // (nothing is cut where no combine follows)
+    a.split_min = item > SHORT ? 4 : 0x7fffffff;  // (nothing is cut where no combine follows)
     // (no hint has a part in what fits the line)
     const int64_t longest = (r.cache_index ? (c.max_context + 127) / 128 : 0) + (int64_t(max_tokens) + 127) / 128;
     if (blocks * c.n_kv_heads * (longest + a.item_cost) > kvc::ROWS_MAX_LINE) return KVC_ERR_UNSUPPORTED;
