@@ -54,20 +54,23 @@ __global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constan
     dev::allow_dependents();
     dev::grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // sequence b's first row, its tokens and its cache position; none where they do not fit
+    auto sequence = [&](int64_t chunk, int b, int &lo, int &n, int &c) {
+        lo = __ldg(a.cu_seqlens + b);
+        const int hi = __ldg(a.cu_seqlens + b + 1);
+        c = a.cache_index ? __ldg(a.cache_index + b) : 0;
+        const bool bad = lo < 0 || hi < lo || hi > a.total || c < 0 || c > a.max_ctx || hi - lo > a.max_ctx - c;
+        if (bad && chunk == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
+        n = bad ? 0 : hi - lo;
+    };
     for (int64_t chunk = blockIdx.x;; chunk += gridDim.x) {
         int64_t base = 0;  // chunks of the sequences before this batch
         bool found = false;
-        for (int b0 = 0; b0 < a.B && !found; b0 += 256) {
+        int b0 = 0;
+        for (; b0 < a.B && !found; b0 += 256) {
             const int b = b0 + threadIdx.x;
             int lo = 0, n = 0, c = 0;
-            if (b < a.B) {
-                lo = __ldg(a.cu_seqlens + b);
-                const int hi = __ldg(a.cu_seqlens + b + 1);
-                c = a.cache_index ? __ldg(a.cache_index + b) : 0;
-                const bool bad = lo < 0 || hi < lo || hi > a.total || c < 0 || c > a.max_ctx || hi - lo > a.max_ctx - c;
-                if (bad && chunk == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
-                n = bad ? 0 : hi - lo;
-            }
+            if (b < a.B) sequence(chunk, b, lo, n, c);
             const int mine = (n + TOKENS - 1) / TOKENS;
             int incl = mine;
 #pragma unroll
@@ -94,6 +97,11 @@ __global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constan
             base += all;
             found = chunk < base;
         }
+        if (chunk == 0)  // the sequences behind the batch that holds the first chunk: recorded too
+            for (int b = b0 + threadIdx.x; b < a.B; b += 256) {
+                int lo, n, c;
+                sequence(chunk, b, lo, n, c);
+            }
         if (!found) return;
         __syncthreads();
         const int t0 = found_s[1], nt = found_s[2];

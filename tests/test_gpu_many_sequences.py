@@ -1,0 +1,43 @@
+"""The serving calls with many sequences: more than one step of a kernel's
+search takes."""
+import numpy as np
+import pytest
+import torch
+
+from tests import _rows
+from tests.test_gpu_ingest import _expect, _snapshot
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,paged", [("bf16", False), ("bf16", True), ("int8", False)])
+@pytest.mark.parametrize("wrong", ["range", "index", "room"])
+def test_packed_append_records_a_late_bad_sequence(dtype, paged, wrong):
+    """600 sequences with valid rows on both sides of a bad one that is not among
+    the first 256: it is skipped and recorded, the others are stored."""
+    B, bad = 600, 300
+    c = _rows.Cache(dtype, 1, B, 4, 2, 128, 32, paged=paged, seed=7)
+    rng = np.random.default_rng(17)
+    lens = rng.integers(0, 12, B)
+    at = rng.integers(0, 21, B)
+    lens[:3], lens[bad], lens[bad + 1], lens[-1] = 5, 0 if wrong == "range" else 9, 4, 6
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    total = int(cu[-1])
+    fine = set(range(B)) - {bad}
+    if wrong == "range":      # reversed; the sequence before it then ends past the packed rows
+        cu[bad] = total + 1
+        fine -= {bad - 1}
+    elif wrong == "index":
+        at[bad] = -1
+    else:
+        at[bad] = 24
+    k, v = c.draw(total, 2, 128, tag="k"), c.draw(total, 2, 128, tag="v")
+    want = _snapshot(c)
+    for b in sorted(fine):
+        n = int(cu[b + 1] - cu[b])
+        if n:
+            r = slice(int(cu[b]), int(cu[b + 1]))
+            _expect(c, want, 0, b, list(range(at[b], at[b] + n)), k[r].transpose(0, 1), v[r].transpose(0, 1))
+    assert c.kvc.kvc_append_packed(c.h, 0, k, v, _rows.ints(cu), _rows.ints(at), total, None) == 0
+    assert c.error() == c.kvc.KVC_ERR_DEVICE_INDEX and c.error() == 0
+    assert all(torch.equal(x, y) for x, y in zip(_snapshot(c), want)) and c.intact()
