@@ -454,7 +454,8 @@ kvc_status kvc_pages_reserve(kvc_cache *h, int32_t *block_table, int32_t *refcou
     st = kvc::bind_workspace(h, workspace, ws_bytes, a);
     if (st != KVC_OK) return st;
     const int smem = 4 * (2 * a.B + 1);
-    if (smem > 48 * 1024 &&
+    // (the kernel's own static shared memory counts towards the 48 KB too)
+    if (smem > 47 * 1024 &&
         cudaFuncSetAttribute(kvc::reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (2 * kvc::MAX_SEQS + 1)) != cudaSuccess)
         return KVC_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

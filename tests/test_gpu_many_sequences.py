@@ -41,3 +41,14 @@ def test_packed_append_records_a_late_bad_sequence(dtype, paged, wrong):
     assert c.kvc.kvc_append_packed(c.h, 0, k, v, _rows.ints(cu), _rows.ints(at), total, None) == 0
     assert c.error() == c.kvc.KVC_ERR_DEVICE_INDEX and c.error() == 0
     assert all(torch.equal(x, y) for x, y in zip(_snapshot(c), want)) and c.intact()
+
+
+@pytest.mark.parametrize("B", [1000, 6120, 6130, 6143, 6144, 8192])
+def test_reserve_at_every_count_of_sequences(B):
+    """The ranges of all sequences are in shared memory: below, between and past
+    the sizes at which they need more than a block has without asking."""
+    from tests.test_gpu_pages import Pool
+    p = Pool(L=1, B=B, G=1, D=64, per=1, blocks=B + 3)
+    n = np.random.default_rng(B).integers(0, 17, B)
+    p.reserve([0] * B, n.tolist())
+    p.check()
