@@ -486,9 +486,10 @@ kvc_status kvc_tree_commit(kvc_cache *h, int32_t layer, int32_t n_layers, const 
  * defined exactly: it depends on the state and the arguments, never on timing.
  * A sequence whose arguments are out of range keeps its pages and
  * KVC_ERR_DEVICE_INDEX is recorded.  These calls need a paged handle
- * (KVC_ERR_UNSUPPORTED otherwise) whose device is current, and at most 8192
- * sequences.  Other host errors: KVC_ERR_INVALID,
- * KVC_ERR_ALIGNMENT, KVC_ERR_WORKSPACE, KVC_ERR_CUDA. */
+ * (KVC_ERR_UNSUPPORTED otherwise) whose device is current, and, all but
+ * kvc_pages_copy, at most 8192 sequences and fewer than 2^31 table entries.
+ * Other host errors: KVC_ERR_INVALID, KVC_ERR_ALIGNMENT, KVC_ERR_WORKSPACE,
+ * KVC_ERR_CUDA. */
 
 /* Bytes of workspace of kvc_pages_reserve and kvc_pages_compact (16-byte
  * aligned; not initialised, nothing kept between calls; not for two calls that

@@ -390,7 +390,8 @@ kvc_status pages_args(const kvc_cache *h, PagesArgs &a) {
 kvc_status pages_args(const kvc_cache *h, int32_t *block_table, int32_t *refcount, PagesArgs &a) {
     const kvc_status st = pages_args(h, a);
     if (st != KVC_OK) return st;
-    if (a.B > MAX_SEQS) return KVC_ERR_UNSUPPORTED;
+    // (places in the list of all ranges are 32-bit numbers)
+    if (a.B > MAX_SEQS || int64_t(a.B) * a.max_blocks > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     if (block_table != h->block_table || !refcount) return KVC_ERR_INVALID;
     if (!aligned16(refcount)) return KVC_ERR_ALIGNMENT;
     a.table = block_table;

@@ -52,3 +52,24 @@ def test_reserve_at_every_count_of_sequences(B):
     n = np.random.default_rng(B).integers(0, 17, B)
     p.reserve([0] * B, n.tolist())
     p.check()
+
+
+def test_tables_past_32_bits_are_refused():
+    """8,192 sequences of 262,144 pages are 2^31 table entries."""
+    from static_kv_cache_gb300 import kvc
+    B, T = 8192, 16 * 262144
+    cfg = kvc.make_config(1, B, 4, 2, 64, T, "bf16")
+    K = torch.zeros(1, 4, 2, 16, 64, device="cuda", dtype=torch.bfloat16)
+    x = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kvc.kvc_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    st, h = kvc.kvc_alloc_paged(cfg, K, K.clone(), 4, x, ws, ws.numel())
+    kvc.check(st, "alloc")
+    try:
+        s = torch.empty(kvc.kvc_pages_workspace_bytes(cfg, 4), dtype=torch.uint8, device="cuda")
+        refused = kvc.KVC_ERR_UNSUPPORTED
+        assert kvc.kvc_pages_reserve(h, x, x, x, x, s, s.numel()) == refused
+        assert kvc.kvc_pages_fork(h, x, x, x) == kvc.kvc_pages_free(h, x, x, x) == refused
+        assert kvc.kvc_pages_compact(h, x, x, None, x, s, s.numel()) == refused
+        assert kvc.kvc_get_error(h, None) == 0 and not x.any()
+    finally:
+        kvc.kvc_free(h)
