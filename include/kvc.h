@@ -342,7 +342,8 @@ kvc_status kvc_prefill_attn(kvc_cache *h, int32_t layer, const void *q,
  * caches of every head width and head group kvc_check_config accepts
  * (KVC_ERR_UNSUPPORTED for KVC_INT8).  Arithmetic: fp32 products and
  * accumulation (of operands in the cache's type; softmax probabilities are
- * rounded to a 16-bit cache's type before they meet V), one
+ * rounded to a 16-bit cache's type before they meet V, fp16 ones at 2^7 times
+ * their size, so that those down to 2^-32 of a row's largest count), one
  * round-to-nearest-even at the end.  A 16-bit cache with d_head 64 or 128 runs
  * on the tensor cores, the others on the CUDA cores.
  *

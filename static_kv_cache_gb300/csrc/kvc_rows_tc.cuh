@@ -96,6 +96,11 @@ struct RowsTcCfg {
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // S_A, S_B (128 columns each), O_A, O_B (D each)
     static constexpr float RESCALE_LOG2 = 8.f;
+    // fp16 probabilities are held 2^7 times as large, next to the type's end (at
+    // most 2^(7 + RESCALE_LOG2) of 65504): at their own size those below 2^-25 of the
+    // reference would be zeros for V, though not in the sum, and 32,000 of them
+    // beside one dominant key as much as 2^-10 of the result.
+    static constexpr float P_SHIFT_LOG2_F16 = 7.f;
     static_assert(NS >= 5, "the copy warps' waits (below)");
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
 
@@ -874,7 +879,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         }
                     }
                 }
-                const float negm = m_run == -INFINITY ? 0.f : -m_run;
+                const float negm = m_run == -INFINITY ? 0.f : BF16 ? -m_run : C::P_SHIFT_LOG2_F16 - m_run;
                 const float2 neg2 = make_float2(negm, negm);
                 float2 ps[4] = {l2, make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
