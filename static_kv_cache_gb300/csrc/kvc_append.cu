@@ -18,12 +18,12 @@
 
 namespace kvc {
 
-__global__ void __launch_bounds__(256) append_kernel(uint8_t *__restrict__ K, uint8_t *__restrict__ V,
-                                                     const uint8_t *__restrict__ k_new,
-                                                     const uint8_t *__restrict__ v_new,
-                                                     const int32_t *__restrict__ cache_index, int index_offset,
+__global__ void __launch_bounds__(256) append_kernel(uint8_t *K, uint8_t *V,
+                                                     const uint8_t *k_new,
+                                                     const uint8_t *v_new,
+                                                     const int32_t *cache_index, int index_offset,
                                                      int B, int H_kv, int T_new, int max_ctx, int row_vecs,
-                                                     const int32_t *__restrict__ table, int max_blocks,
+                                                     const int32_t *table, int max_blocks,
                                                      int num_blocks, int32_t *err) {
     dev::grid_dependency_wait();   // the previous kernel on the stream has completed
     dev::allow_dependents();
@@ -37,16 +37,16 @@ __global__ void __launch_bounds__(256) append_kernel(uint8_t *__restrict__ K, ui
         const int64_t seg = r / run;                 // b * H_kv + j
         const int64_t off = r - seg * run;           // vector within the run
         const int b = int(seg / H_kv);
-        const int ci = __ldg(cache_index + b) + index_offset;
+        const uint4 x = dev::ld(reinterpret_cast<const uint4 *>(is_v ? v_new : k_new) + r);  // on its way meanwhile
+        const int ci = dev::ld(cache_index + b) + index_offset;
         if (ci < 0 || ci > max_ctx - T_new) {
             if (off == 0 && seg % H_kv == 0 && !is_v) atomicCAS(err, 0, ERR_DEVICE_INDEX);
             continue;
         }
-        const uint4 *src = reinterpret_cast<const uint4 *>(is_v ? v_new : k_new) + seg * run + off;
         int64_t row;  // destination row, in rows of the layer's cache or pool
         if (table) {  // paged: the position's slot in its physical block of 16 rows
             const int pos = ci + int(off / row_vecs);
-            const int phys = __ldg(table + int64_t(b) * max_blocks + pos / 16);
+            const int phys = dev::ld(table + int64_t(b) * max_blocks + pos / 16);
             if (phys < 0 || phys >= num_blocks) {
                 atomicCAS(err, 0, ERR_DEVICE_INDEX);
                 continue;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256) append_kernel(uint8_t *__restrict__ K, ui
             row = seg * max_ctx + ci + off / row_vecs;
         }
         uint4 *dst = reinterpret_cast<uint4 *>(is_v ? V : K) + row * row_vecs + off % row_vecs;
-        *dst = __ldg(src);
+        *dst = x;
     }
 }
 
@@ -67,11 +67,11 @@ __global__ void __launch_bounds__(256) append_kernel(uint8_t *__restrict__ K, ui
 // scale 0.  One warp per (row, K or V): lane l holds elements
 // [l * D/32, (l + 1) * D/32).
 template <int D>
-__global__ void __launch_bounds__(256) append_q8_kernel(uint8_t *__restrict__ K, uint8_t *__restrict__ V,
-                                                        float *__restrict__ ks, float *__restrict__ vs,
-                                                        const uint8_t *__restrict__ k_new,
-                                                        const uint8_t *__restrict__ v_new,
-                                                        const int32_t *__restrict__ cache_index,
+__global__ void __launch_bounds__(256) append_q8_kernel(uint8_t *K, uint8_t *V,
+                                                        float *ks, float *vs,
+                                                        const uint8_t *k_new,
+                                                        const uint8_t *v_new,
+                                                        const int32_t *cache_index,
                                                         int index_offset, int B, int H_kv, int T_new, int max_ctx,
                                                         int32_t *err) {
     constexpr int EPL = D / 32;  // bf16 elements per lane (2 or 4)
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) append_q8_kernel(uint8_t *__restrict__ K,
         const int64_t seg = r / T_new;
         const int t = int(r - seg * T_new);
         const int b = int(seg / H_kv);
-        const int ci = __ldg(cache_index + b) + index_offset;
+        const int ci = dev::ld(cache_index + b) + index_offset;
         if (ci < 0 || ci > max_ctx - T_new) {
             if (lane == 0 && t == 0 && seg % H_kv == 0 && !is_v) atomicCAS(err, 0, ERR_DEVICE_INDEX);
             continue;

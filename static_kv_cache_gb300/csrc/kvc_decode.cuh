@@ -375,7 +375,7 @@ __device__ __forceinline__ void merge_piece(const DecodeArgs &a, const Plan &pla
         for (int i = ctid; i < 2 * VECS; i += NW * 32) {
             const bool is_v = i >= VECS;
             const int v = is_v ? i - VECS : i;
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) +
+            const uint4 x = dev::ld(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) +
                                                                   int64_t(seg) * D * int64_t(sizeof(T))) + v);
             reinterpret_cast<uint4 *>(const_cast<uint8_t *>(is_v ? a.V : a.K) + row_off)[v] = x;
         }
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(DecodeCfg<T, D, G>::THREADS, 1)
             for (int h = 0; h < G; ++h) {
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
-                    const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(qb + h * D) + sub + c * LPR);
+                    const uint4 raw = dev::ld(reinterpret_cast<const uint4 *>(qb + h * D) + sub + c * LPR);
                     Ops::unpack2(raw, &qr[h][c * PC]);
                 }
 #pragma unroll

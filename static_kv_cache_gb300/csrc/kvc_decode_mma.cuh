@@ -266,7 +266,7 @@ __device__ __forceinline__ uint32_t produce_tiles_paged(const DecodeArgs &a, Wal
         // first + 2t + 1, both in window t / 16; window k + 1 is loaded when
         // window k comes into use, so its latency hides behind 16 tiles.
         const int first = pc.lo / BS;
-        auto load_window = [&](int base) { return base + lane < a.max_blocks ? __ldg(trow + base + lane) : -1; };
+        auto load_window = [&](int base) { return base + lane < a.max_blocks ? dev::ld(trow + base + lane) : -1; };
         int32_t cached = load_window(first);
         int32_t ahead = load_window(first + 32);
         int cached_base = first;
@@ -400,7 +400,7 @@ __device__ __forceinline__ uint32_t produce_tiles_paged_pair(const DecodeArgs &a
         // the tile's table entry, loaded one tile ahead (a warp-uniform load
         // from the table's cached lines) so that its latency hides behind
         // the previous tile's copies
-        int phys_next = __ldg(trow + first);
+        int phys_next = dev::ld(trow + first);
         for (int row0 = pc.lo; row0 < pc.hi; row0 += BS) {
             const int nr = min(BS, pc.hi - row0);
             const int blk = row0 / BS;
@@ -424,7 +424,7 @@ __device__ __forceinline__ uint32_t produce_tiles_paged_pair(const DecodeArgs &a
                     break;
                 }
             }
-            phys_next = blk + 1 < a.max_blocks ? __ldg(trow + blk + 1) : -1;
+            phys_next = blk + 1 < a.max_blocks ? dev::ld(trow + blk + 1) : -1;
             const uint32_t full = bar0 + 8 * stage;
             const uint32_t kdst = stage0 + uint32_t(stage) * C::STAGE_BYTES;
             const uint32_t vdst = kdst + C::TILE_BYTES;
@@ -711,11 +711,11 @@ __device__ __forceinline__ bool merge_pieces(const DecodeArgs &a, const Plan &pl
                 const int kvh = pc.kv * KH + z;  // KV head
                 const int64_t seg = int64_t(pc.b) * a.H_kv * KH + kvh;
                 const uint4 v =
-                    __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) + seg * ROW_BYTES) + c16);
+                    dev::ld(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) + seg * ROW_BYTES) + c16);
                 int64_t row_off = seg * kv_slab + int64_t(pc.n - 1) * ROW_BYTES;
                 if (a.block_table) {  // paged: the row's slot in its physical block
                     const int p = pc.n - 1;
-                    const int phys = __ldg(a.block_table + int64_t(pc.b) * a.max_blocks + p / 16);
+                    const int phys = dev::ld(a.block_table + int64_t(pc.b) * a.max_blocks + p / 16);
                     row_off = phys >= 0 && phys < a.num_blocks
                                   ? ((int64_t(phys) * a.H_kv * KH + kvh) * 16 + p % 16) * ROW_BYTES
                                   : -1;  // reported by the producer
@@ -807,12 +807,12 @@ __device__ __forceinline__ void merge_pieces_chunked(const DecodeArgs &a, const 
             const int64_t seg = int64_t(pc.b) * a.H_kv + pc.kv;
             const bool is_v = lane >= CHUNKS;
             const int c16 = is_v ? lane - CHUNKS : lane;
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) + seg * ROW_BYTES) + c16);
+            const uint4 v = dev::ld(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) + seg * ROW_BYTES) + c16);
             uint8_t *cache = const_cast<uint8_t *>(is_v ? a.V : a.K);
             int64_t row_off = seg * kv_slab + int64_t(pc.n - 1) * ROW_BYTES;
             if (a.block_table) {
                 const int p = pc.n - 1;
-                const int phys = __ldg(a.block_table + int64_t(pc.b) * a.max_blocks + p / 16);
+                const int phys = dev::ld(a.block_table + int64_t(pc.b) * a.max_blocks + p / 16);
                 row_off = phys >= 0 && phys < a.num_blocks
                               ? ((int64_t(phys) * a.H_kv + pc.kv) * 16 + p % 16) * ROW_BYTES
                               : -1;
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(MmaCfg<T, D, G>::THREADS, 1)
     dev::grid_dependency_wait();
     dev::allow_dependents();
     if (a.B <= C::VL_CACHE)
-        for (int b = threadIdx.x; b < a.B; b += C::THREADS) vl_cache[b] = __ldg(a.valid_len + b);
+        for (int b = threadIdx.x; b < a.B; b += C::THREADS) vl_cache[b] = dev::ld(a.valid_len + b);
     __syncthreads();
 
     if (warp == C::IDLE_WARP) return;
@@ -1062,8 +1062,8 @@ __global__ void __launch_bounds__(MmaCfg<T, D, G>::THREADS, 1)
                 const bool qv = hq < G;
 #pragma unroll
                 for (int ks = 0; ks < KSTEPS; ++ks) {
-                    qb[ks][nt][0] = qv ? __ldg(reinterpret_cast<const uint32_t *>(qrow + ks * 16 + 2 * tq)) : 0u;
-                    qb[ks][nt][1] = qv ? __ldg(reinterpret_cast<const uint32_t *>(qrow + ks * 16 + 8 + 2 * tq)) : 0u;
+                    qb[ks][nt][0] = qv ? dev::ld(reinterpret_cast<const uint32_t *>(qrow + ks * 16 + 2 * tq)) : 0u;
+                    qb[ks][nt][1] = qv ? dev::ld(reinterpret_cast<const uint32_t *>(qrow + ks * 16 + 8 + 2 * tq)) : 0u;
                 }
 #pragma unroll
                 for (int mt = 0; mt < KSTEPS; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;

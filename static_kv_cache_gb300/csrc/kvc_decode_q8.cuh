@@ -211,7 +211,7 @@ __device__ __forceinline__ uint32_t produce_tiles_q8(const DecodeArgs &a, Walker
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const uint8_t *src = (t ? a.v_new : a.k_new) + int64_t(seg) * (2 * C::ROW_BYTES) + 8 * lane;
-                        const uint2 raw = __ldg(reinterpret_cast<const uint2 *>(src));
+                        const uint2 raw = dev::ld(reinterpret_cast<const uint2 *>(src));
                         const float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
                                             __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
                         float scale;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, G>::THREADS, 1) decode_q8_kernel(cons
     dev::grid_dependency_wait();
     dev::allow_dependents();
     if (a.B <= C::VL_CACHE)
-        for (int b = threadIdx.x; b < a.B; b += C::THREADS) vl_cache[b] = __ldg(a.valid_len + b);
+        for (int b = threadIdx.x; b < a.B; b += C::THREADS) vl_cache[b] = dev::ld(a.valid_len + b);
     __syncthreads();
 
     if (warp == C::IDLE_WARP) return;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, G>::THREADS, 1) decode_q8_kernel(cons
             for (int cp = 0; cp < CPAIRS; ++cp) {
                 const int d0 = 32 * cp + 4 * tq;
                 auto ld = [&](int d) {
-                    return gq < G ? q8::f16x2_from_bf16x2(__ldg(reinterpret_cast<const uint32_t *>(qrow + d))) : 0u;
+                    return gq < G ? q8::f16x2_from_bf16x2(dev::ld(reinterpret_cast<const uint32_t *>(qrow + d))) : 0u;
                 };
                 qb[cp][0] = ld(d0);
                 qb[cp][1] = ld(d0 + 16);

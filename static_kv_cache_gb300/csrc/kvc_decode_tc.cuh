@@ -437,7 +437,7 @@ __global__ void __maxnreg__(128) decode_tc_kernel(const __grid_constant__ Decode
                             const uint8_t *src = row0 + r == new_row
                                                      ? new_src
                                                      : src_seg + int64_t(row0 + r) * C::ROW_BYTES;
-                            v = __ldg(reinterpret_cast<const uint4 *>(src) + c16);
+                            v = dev::ld(reinterpret_cast<const uint4 *>(src) + c16);
                         }
                         dev::st_shared_v4(C::swz(dst, r, c16), v);
                     }
@@ -551,7 +551,7 @@ __global__ void __maxnreg__(128) decode_tc_kernel(const __grid_constant__ Decode
                     const int h = i / C::CHUNKS, c16 = i % C::CHUNKS;
                     dev::st_shared_v4(q_s + uint32_t(c16 >> 3) * C::QB + uint32_t(h) * 128 +
                                           (uint32_t((c16 & 7) ^ (h & 7)) << 4),
-                                      __ldg(qg + i));
+                                      dev::ld(qg + i));
                 }
                 dev::fence_proxy_async_smem();
                 __syncwarp();
@@ -705,7 +705,7 @@ __global__ void __maxnreg__(128) decode_tc_kernel(const __grid_constant__ Decode
             if (a.k_new && pc.hi == pc.n && sid < 2 * C::CHUNKS) {
                 const bool is_v = sid >= C::CHUNKS;
                 const int c16 = is_v ? sid - C::CHUNKS : sid;
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) +
+                const uint4 v = dev::ld(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) +
                                                                        int64_t(seg) * C::ROW_BYTES) + c16);
                 uint8_t *cache = const_cast<uint8_t *>(is_v ? a.V : a.K);  // the caller's writable cache
                 reinterpret_cast<uint4 *>(cache + int64_t(seg) * kv_slab + int64_t(pc.n - 1) * C::ROW_BYTES)[c16] = v;

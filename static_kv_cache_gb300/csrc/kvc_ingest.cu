@@ -22,7 +22,7 @@ __device__ __forceinline__ bool cache_row(const IngestArgs &a, int b, int pos, i
         head_step = a.max_ctx;
         return true;
     }
-    const int phys = __ldg(a.block_table + int64_t(b) * a.max_blocks + pos / 16);
+    const int phys = dev::ld(a.block_table + int64_t(b) * a.max_blocks + pos / 16);
     row = int64_t(phys) * a.H_kv * 16 + pos % 16;
     head_step = 16;
     return phys >= 0 && phys < a.num_blocks;
@@ -56,9 +56,9 @@ __global__ void __launch_bounds__(256) append_packed_kernel(const __grid_constan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // sequence b's first row, its tokens and its cache position; none where they do not fit
     auto sequence = [&](int64_t chunk, int b, int &lo, int &n, int &c) {
-        lo = __ldg(a.cu_seqlens + b);
-        const int hi = __ldg(a.cu_seqlens + b + 1);
-        c = a.cache_index ? __ldg(a.cache_index + b) : 0;
+        lo = dev::ld(a.cu_seqlens + b);
+        const int hi = dev::ld(a.cu_seqlens + b + 1);
+        c = a.cache_index ? dev::ld(a.cache_index + b) : 0;
         const bool bad = lo < 0 || hi < lo || hi > a.total || c < 0 || c > a.max_ctx || hi - lo > a.max_ctx - c;
         if (bad && chunk == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
         n = bad ? 0 : hi - lo;
@@ -164,12 +164,12 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
     const unsigned u = blockIdx.x * 8 + (threadIdx.x >> 5);  // (sequence, KV head, chunk)
     if (u >= segs * chunks) return;
     const unsigned seg = u / chunks, chunk = u - seg * chunks, b = seg / a.H_kv, kv = seg - b * a.H_kv;
-    const int n = __ldg(a.n_accept + b), c = __ldg(a.cache_index + b), i0 = int(chunk) * STEPS;
+    const int n = dev::ld(a.n_accept + b), c = dev::ld(a.cache_index + b), i0 = int(chunk) * STEPS;
     bool bad = n < 0 || n > a.P || c < 0 || c > a.max_ctx || n > a.max_ctx - c;
     int node = 0;  // path entry 32 (i0 / 32) + lane
     if (!bad && (i0 < n || chunk == 0)) {
         for (int i = lane; i < n; i += 32) {
-            const int s = __ldg(a.path + int64_t(b) * a.P + i);
+            const int s = dev::ld(a.path + int64_t(b) * a.P + i);
             bad = bad || s < 0 || s >= a.T;
             if (i / 32 == i0 / 32) node = s;
         }
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
                 const int64_t d = __shfl_sync(0xffffffffu, to, i), f = __shfl_sync(0xffffffffu, from, i);
                 at[e] = x < vecs && d >= 0 ? d * a.row_vecs + w : -1;
                 if (at[e] >= 0) {
-                    k[e] = __ldg(reinterpret_cast<const uint4 *>(a.k_new) + f * a.row_vecs + w);
-                    v[e] = __ldg(reinterpret_cast<const uint4 *>(a.v_new) + f * a.row_vecs + w);
+                    k[e] = dev::ld(reinterpret_cast<const uint4 *>(a.k_new) + f * a.row_vecs + w);
+                    v[e] = dev::ld(reinterpret_cast<const uint4 *>(a.v_new) + f * a.row_vecs + w);
                 }
             }
 #pragma unroll

@@ -584,6 +584,15 @@ __device__ __forceinline__ void record_error(int32_t *err, int32_t code) {
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Global memory that a kernel of this library may read was written by the
+// kernels before it -- tables, lengths, rows, queries, partial results -- while
+// this one was already resident.  It is not read-only for the kernel's lifetime,
+// as the read-only path (ld.global.nc: the read-only load intrinsic, or const
+// pointers with restrict) demands: that path may serve a line from before the
+// write, and its loads may move ahead of the wait.  So: plain loads.
+template <typename V>
+__device__ __forceinline__ V ld(const V *p) { return *p; }
+
 // The int8 cache's quantisation of one row ("10.3 -- KV cache implementation
 // details", section 4.4: the cache stored as int8, p = 1), taken by a whole
 // warp: lane l holds elements [l * EPL, (l + 1) * EPL) of the row in fp32.

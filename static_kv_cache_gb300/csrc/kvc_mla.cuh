@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(128) mla_absorb_kernel(const MlaAbsorbArgs a) 
         for (int i = t; i < 64 * 8; i += 128) {
             const int bb = i >> 3, c = (i & 7) * 8, b = b0 + bb;
             if (b >= a.B) break;
-            const int v = __ldg(a.valid_len + b);
+            const int v = dev::ld(a.valid_len + b);
             if (v >= 1 && v <= a.max_ctx)
                 *reinterpret_cast<uint4 *>(cache + (int64_t(b) * a.max_ctx + v - 1) * DC + j0 + c) =
-                    __ldg(reinterpret_cast<const uint4 *>(cn + int64_t(b) * DC + j0 + c));
+                    dev::ld(reinterpret_cast<const uint4 *>(cn + int64_t(b) * DC + j0 + c));
             else if (c == 0 && blockIdx.y == 0)
                 dev::record_error(a.err, ERR_DEVICE_INDEX);
         }
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(MlaCfg<T, DC, H>::THREADS, 1) mla_decode_kerne
                 reinterpret_cast<const uint4 *>(static_cast<const T *>(a.qt) + (int64_t(pc.b) * a.H_all + head0) * DC);
             for (int i = ctid; i < H * DC / 8; i += NW * 32) {
                 const int h = i / (DC / 8), c = i - h * (DC / 8);
-                *reinterpret_cast<uint4 *>(q_s + h * C::QS + c * 8) = __ldg(src + i);
+                *reinterpret_cast<uint4 *>(q_s + h * C::QS + c * 8) = dev::ld(src + i);
             }
         }
         dev::named_barrier_sync(1, NW * 32);
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(512) mla_combine_kernel(const MlaCombineArgs a
                     wk[kk] = k < ns ? wk_s[k] : 0.f;
 #pragma unroll
                     for (int r = 0; r < R4; ++r)
-                        x[kk][r] = wk[kk] != 0.f ? __ldg(reinterpret_cast<const float4 *>(acc + k * acc_stride + r * 128))
+                        x[kk][r] = wk[kk] != 0.f ? dev::ld(reinterpret_cast<const float4 *>(acc + k * acc_stride + r * 128))
                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll

@@ -45,7 +45,7 @@ __device__ __forceinline__ int entry(const PagesArgs &a, int x) {
 // A block owns `cols` columns of the table: it keeps all B rows of them in
 // shared memory, so that the gather over parents can go in place.  Counts
 // change only where an entry does; integer sums do not depend on their order.
-__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesArgs a, const int32_t *__restrict__ parent,
+__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesArgs a, const int32_t *parent,
                                                    int cols) {
     extern __shared__ int32_t old[];  // [B][cols]
     dev::allow_dependents();
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
     __syncthreads();
     for (int x = threadIdx.x; x < a.B * nc; x += blockDim.x) {
         const int b = x / nc, j = x - b * nc;
-        const int p = __ldg(parent + b);
+        const int p = dev::ld(parent + b);
         if (p < -1 || p >= a.B) {
             dev::record_error(a.err, ERR_DEVICE_INDEX);
             continue;
@@ -73,13 +73,13 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
 }
 
 // ---- free ------------------------------------------------------------------
-__global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ PagesArgs a, const int32_t *__restrict__ keep) {
+__global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ PagesArgs a, const int32_t *keep) {
     dev::allow_dependents();
     dev::grid_dependency_wait();
     const int64_t total = int64_t(a.B) * a.max_blocks;
     for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < total; x += int64_t(gridDim.x) * blockDim.x) {
         const int b = int(x / a.max_blocks), j = int(x - int64_t(b) * a.max_blocks);
-        const int n = __ldg(keep + b);
+        const int n = dev::ld(keep + b);
         if (n < 0 || n > a.max_ctx) {
             if (j == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
             continue;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ P
         const int b = b0 + tid;
         int j0 = 0, length = 0;
         if (b < a.B) {
-            const int len = __ldg(r.len + b), grown = __ldg(r.new_len + b);
+            const int len = dev::ld(r.len + b), grown = dev::ld(r.new_len + b);
             bool ok = len >= 0 && grown >= len && grown <= a.max_ctx;
             j0 = ok ? len / PAGE : 0;
             if (ok && grown > len) {
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ P
         a.refs[page] = 1;
         if (entry(a, was) < 0) continue;
         atomicSub(a.refs + was, 1);
-        const int len = __ldg(r.len + b);
+        const int len = dev::ld(r.len + b);
         if (j == len / PAGE && len % PAGE != 0) {  // (at most one page of a sequence)
             const int c = atomicAdd(&copies, 1);
             a.src[c] = was;

@@ -150,7 +150,7 @@ __device__ __forceinline__ bool prefill_item(const A &a, int k, int tokens_per_i
     it.kv = it.seg % a.H_kv;
     it.t0 = it.qb * tokens_per_item;
     it.ntok = min(tokens_per_item, a.T_new - it.t0);
-    it.c = __ldg(a.cache_index + it.b);
+    it.c = dev::ld(a.cache_index + it.b);
     const bool bad = it.c < 0 || it.c > a.max_ctx - a.T_new;
     it.kend = it.c + it.t0 + it.ntok;  // keys [0, kend) are visible to some row of the item
     it.ntiles = bad ? 0 : (it.kend + 127) / 128;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(TcPrefillCfg<T, D>::THREADS, 1)
             for (int i = lane; i < (BN - boxed) * C::CHUNKS; i += 32) {
                 const int r = boxed + i / C::CHUNKS, c16 = i % C::CHUNKS;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r < nr) v = __ldg(reinterpret_cast<const uint4 *>(src + int64_t(r) * C::ROW_BYTES) + c16);
+                if (r < nr) v = dev::ld(reinterpret_cast<const uint4 *>(src + int64_t(r) * C::ROW_BYTES) + c16);
                 dev::st_shared_v4(C::swz(dst, r, c16), v);
             }
             dev::fence_proxy_async_smem();  // the tensor core reads these rows
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(TcPrefillCfg<T, D>::THREADS, 1)
                 else if (async)
                     dev::cp_async_16(C::swz(qt, r, c16), qrow + c16);
                 else
-                    dev::st_shared_v4(C::swz(qt, r, c16), __ldg(qrow + c16));
+                    dev::st_shared_v4(C::swz(qt, r, c16), dev::ld(qrow + c16));
             }
         };
         bool ok = true;

@@ -41,16 +41,16 @@ struct RowsSeq {
 
 __device__ __forceinline__ RowsSeq rows_seq(const RowsArgs &a, int b) {
     RowsSeq s;
-    s.c = a.cache_index ? __ldg(a.cache_index + b) : 0;
+    s.c = a.cache_index ? dev::ld(a.cache_index + b) : 0;
     s.bad = s.c < 0 || s.c > a.max_ctx;
     s.row0 = 0;
     if (a.cu_seqlens) {
-        const int lo = __ldg(a.cu_seqlens + b), hi = __ldg(a.cu_seqlens + b + 1);
+        const int lo = dev::ld(a.cu_seqlens + b), hi = dev::ld(a.cu_seqlens + b + 1);
         s.bad = s.bad || lo < 0 || hi < lo || hi > a.total;
         s.row0 = lo;
         s.n = s.bad ? 0 : hi - lo;
     } else {
-        s.n = a.n_nodes ? __ldg(a.n_nodes + b) : a.T;
+        s.n = a.n_nodes ? dev::ld(a.n_nodes + b) : a.T;
         s.bad = s.bad || s.n < 0 || s.n > a.T;
         if (s.bad) s.n = 0;
     }

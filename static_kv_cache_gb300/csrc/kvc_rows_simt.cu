@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
                         kp = static_cast<const uint8_t *>(a.k_new), vp = static_cast<const uint8_t *>(a.v_new);
                         row = rows_offset(a, s, b, a.H_kv, kv, key - s.c, 1);
                     } else if (a.block_table) {
-                        const int phys = __ldg(a.block_table + int64_t(b) * a.max_blocks + key / 16);
+                        const int phys = dev::ld(a.block_table + int64_t(b) * a.max_blocks + key / 16);
                         if (phys < 0 || phys >= a.num_blocks)
                             dev::record_error(a.err, ERR_DEVICE_INDEX);
                         else
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
                         row = (int64_t(b) * a.H_kv + kv) * a.max_ctx + key;
                     }
                     if (row >= 0) {
-                        kk = __ldg(reinterpret_cast<const uint4 *>(kp) + row * CH + c16);
-                        vv = __ldg(reinterpret_cast<const uint4 *>(vp) + row * CH + c16);
+                        kk = dev::ld(reinterpret_cast<const uint4 *>(kp) + row * CH + c16);
+                        vv = dev::ld(reinterpret_cast<const uint4 *>(vp) + row * CH + c16);
                     }
                 }
                 ks[j * (CH + 1) + c16] = kk;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
                 bool see = tok[k] >= 0 && key < end;
                 if (see && key >= s.c) {
                     const int sn = key - s.c;
-                    see = a.tree_mask ? (__ldg(a.tree_mask + (int64_t(b) * a.T + tok[k]) * a.mask_words + (sn >> 5)) >> (sn & 31)) & 1
+                    see = a.tree_mask ? (dev::ld(a.tree_mask + (int64_t(b) * a.T + tok[k]) * a.mask_words + (sn >> 5)) >> (sn & 31)) & 1
                                       : sn <= tok[k];
                 }
                 const float x = see ? sc[k] : -INFINITY;

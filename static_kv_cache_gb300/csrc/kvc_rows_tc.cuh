@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                 auto page_of = [&](int jt) {
                     const int blk = 8 * jt + lane;
                     if (!a.block_table || lane >= 8 || jt >= it.np || blk * 16 >= it.c) return 0;
-                    return __ldg(a.block_table + int64_t(it.b) * a.max_blocks + blk);
+                    return dev::ld(a.block_table + int64_t(it.b) * a.max_blocks + blk);
                 };
                 int next_page = page_of(it.j0);
                 for (int j = 0; j < n; ++j) {
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                             w[q] = lead_word(nv, q);
                         else if (a.tree_mask)
                             w[q] = row_ok && key0 / 32 + q < a.mask_words
-                                       ? __ldg(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + key0 / 32 + q) & lead_word(nv, q)
+                                       ? dev::ld(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + key0 / 32 + q) & lead_word(nv, q)
                                        : 0u;
                         else
                             w[q] = lead_word(min(nv, t - key0 + 1), q);
@@ -1035,7 +1035,7 @@ __global__ void __launch_bounds__(RowsTcCfg<D>::THREADS, 1) rows_tc_kernel(const
                         const int key0 = 128 * (jt - it.np), nv = min(128, it.vis - key0);
                         if (!(nv < 128 || a.tree_mask || key0 + 127 > it.t0)) continue;
                         for (int key = key0; key < key0 + nv; ++key) {
-                            const bool see = a.tree_mask ? __ldg(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + (key >> 5)) >> (key & 31) & 1u
+                            const bool see = a.tree_mask ? dev::ld(a.tree_mask + (int64_t(it.b) * a.T + t) * a.mask_words + (key >> 5)) >> (key & 31) & 1u
                                                          : key <= t;
                             if (!see) continue;
                             const T *v = reinterpret_cast<const T *>(a.v_new) + rows_offset(a, sq, it.b, a.H_kv, it.kv, key, D) + 32 * q;
