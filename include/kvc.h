@@ -383,8 +383,7 @@ uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
  *                skipped (its output rows are left unwritten) and
  *                KVC_ERR_DEVICE_INDEX is recorded.  Packed rows outside every
  *                sequence are left unwritten; rows that two ranges share (which
- *                takes a reversed one) get either sequence's output, or, where
- *                the ranges together pass the limit below, none is written
+ *                takes a reversed one) get either sequence's output
  *   cache_index  device int32 [B]: cached rows of each sequence, or NULL: no
  *                sequence has any.  Outside [0, max_context]: skipped and
  *                recorded like a bad range.
@@ -393,8 +392,14 @@ uint64_t kvc_rows_workspace_bytes(const kvc_config *cfg);
  *   out          device, [total, H, d_h], 16-byte aligned
  * Paged handles: a block-table entry outside [0, num_blocks) among a
  * sequence's cached rows records KVC_ERR_DEVICE_INDEX; that sequence's output
- * is then undefined.  KVC_ERR_UNSUPPORTED also for a call whose product of
- * query blocks and key tiles passes 2000 * 2^20 (over a million packed tokens).
+ * is then undefined.
+ * Limit of one call on the tensor cores: 2000 * 2^20 steps, where a block of
+ * 2 * floor(128 / g) tokens of a sequence takes, per KV head, three steps and one
+ * for each tile of 128 keys that it sees (a prompt of n tokens about
+ * n_heads * n^2 / 65,536: 2 million tokens at 32 heads).  The steps of the
+ * sequences as given count, not those of total or max_context.  A call past the
+ * limit records KVC_ERR_DEVICE_INDEX and writes nothing.  KVC_ERR_UNSUPPORTED
+ * also where max_context > 2^31 - 257.
  * Host errors: KVC_ERR_INVALID, KVC_ERR_UNSUPPORTED, KVC_ERR_ALIGNMENT,
  * KVC_ERR_WORKSPACE, KVC_ERR_CUDA. */
 kvc_status kvc_prompt_attn(kvc_cache *h, int32_t layer, const void *q, const void *k, const void *v,
@@ -443,7 +448,7 @@ kvc_status kvc_append_packed(kvc_cache *h, int32_t layer, const void *k, const v
  *                 the launch
  *   workspace     device, ws_bytes >= kvc_rows_workspace_bytes(cfg)
  *   out           device, [B, H, T, d_h], 16-byte aligned
- * Paged handles and host errors as for kvc_prompt_attn. */
+ * Paged handles, limit and host errors as for kvc_prompt_attn. */
 kvc_status kvc_tree_attn(kvc_cache *h, int32_t layer, const void *q, const void *k_new,
                          const void *v_new, const int32_t *cache_index, const int32_t *n_nodes,
                          const uint32_t *tree_mask, int32_t T, int32_t max_index_hint,

@@ -73,6 +73,7 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
         const cudaError_t e = kvc::launch_rows_simt(r, c.dtype, c.d_head, max_tokens, s);
         return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
     }
+    if (c.max_context > 0x7fffffff - 256) return KVC_ERR_UNSUPPORTED;  // (a tile's last row is a 32-bit number)
     kvc::RowsTcArgs a{};
     static_cast<kvc::RowsArgs &>(a) = r;
     if (!encode_new_rows(h, r, r.k_new, &a.tm_k_new) || !encode_new_rows(h, r, r.v_new, &a.tm_v_new) ||
@@ -89,7 +90,9 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     a.cuts = reinterpret_cast<kvc::RowsCut *>(ws);
     a.part_ml = reinterpret_cast<float *>(ws + ml);
     a.part_acc = reinterpret_cast<float *>(ws + acc);
-    // at most so many key tiles of one item, and length of the whole line
+    // at most so many key tiles of one item, and length of the whole line (these
+    // size the launch; what fits the line's limit is seen on the device, from the
+    // sequences' own lengths)
     const int ti = 2 * (128 / h->group);
     const int64_t item = (max_cached + 127) / 128 + (int64_t(max_tokens) + 127) / 128;
     const int64_t blocks = r.cu_seqlens ? r.total / ti + (c.batch < r.total ? c.batch : r.total)
@@ -105,9 +108,6 @@ kvc_status launch_rows(kvc_cache *h, const kvc::RowsArgs &r, int max_tokens, int
     constexpr int SHORT = 8;
     a.min_share = 4;
     a.split_min = item > SHORT ? 4 : 0x7fffffff;  // (nothing is cut where no combine follows)
-    // (no hint has a part in what fits the line)
-    const int64_t longest = (r.cache_index ? (c.max_context + 127) / 128 : 0) + (int64_t(max_tokens) + 127) / 128;
-    if (blocks * c.n_kv_heads * (longest + a.item_cost) > kvc::ROWS_MAX_LINE) return KVC_ERR_UNSUPPORTED;
     const int64_t line = blocks * c.n_kv_heads * (item + a.item_cost);
     int64_t grid = h->num_sms < kvc::ROWS_MAX_CTAS ? h->num_sms : kvc::ROWS_MAX_CTAS;
     if ((line + a.min_share - 1) / a.min_share < grid) grid = (line + a.min_share - 1) / a.min_share;

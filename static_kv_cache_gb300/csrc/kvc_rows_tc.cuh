@@ -156,27 +156,29 @@ static_assert(sizeof(RowsItem) <= 64, "item slot");
 // Length on the line of the first q token blocks (of ti tokens) of one KV head
 // of a sequence: a.item_cost each for an item's start and end, and its key
 // tiles -- the cached ones, and of the new ones all under a mask, otherwise
-// those up to its last token.  (The host keeps the line of sequences that share
-// no rows below ROWS_MAX_LINE.)
-__device__ __forceinline__ int rows_prefix(const RowsTcArgs &a, const RowsSeq &s, int ti, int q) {
-    const int base = q * (a.item_cost + (s.c + 127) / 128), kt = (s.n + 127) / 128;
+// those up to its last token.  (Int: 64 bits where the line is measured, 32 in
+// one that is known to stay below ROWS_MAX_LINE.)
+template <typename Int>
+__device__ __forceinline__ Int rows_prefix(const RowsTcArgs &a, const RowsSeq &s, int ti, int q) {
+    const Int base = Int(q) * (a.item_cost + (s.c + 127) / 128), kt = (s.n + 127) / 128;
     if (a.tree_mask) return base + q * kt;
     if (ti > 128) {  // 256 tokens: block k (from 1) sees 2 k tiles, the last one kt
-        const int nblk = (s.n + ti - 1) / ti;
-        return base + (q < nblk ? q * (q + 1) : nblk * (nblk - 1) + kt);
+        const Int nblk = (s.n + ti - 1) / ti;
+        return base + (q < nblk ? Int(q) * (q + 1) : nblk * (nblk - 1) + kt);
     }
     const int m = 128 / ti;
     if (m * ti == 128) {  // m blocks a tile
-        const int full = q / m, rest = q - full * m;
+        const Int full = q / m, rest = q - full * m;
         return base + m * full * (full + 1) / 2 + rest * (full + 1);
     }
-    int sum = base;
+    Int sum = base;
     for (int k = 1; k <= q; ++k) sum += (min(s.n, k * ti) + 127) / 128;
     return sum;
 }
 
-__device__ __forceinline__ int rows_seq_length(const RowsTcArgs &a, const RowsSeq &s, int ti) {
-    return s.n == 0 ? 0 : rows_prefix(a, s, ti, (s.n + ti - 1) / ti);
+template <typename Int>
+__device__ __forceinline__ Int rows_seq_length(const RowsTcArgs &a, const RowsSeq &s, int ti) {
+    return s.n == 0 ? 0 : rows_prefix<Int>(a, s, ti, (s.n + ti - 1) / ti);
 }
 
 __device__ __forceinline__ int rows_block_tiles(const RowsArgs &a, const RowsSeq &s, int ti, int qb) {
@@ -211,10 +213,13 @@ struct RowsPlace {
 __device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane, int &share, int &begin, int &end, RowsPlace &place) {
     constexpr unsigned FULL = 0xffffffffu;
     int mine = 0;  // length of this lane's sequence (of the last batch of 32)
-    int64_t sum = 0;
-    for (int i = lane; i < a.B; i += 32) sum += mine = rows_seq_length(a, rows_seq(a, i), ti) * a.H_kv;
-    // Sequences that share packed rows (their ranges are not in order) can be longer
-    // together than the host's bound, ROWS_MAX_LINE: then no item is taken.
+    int64_t sum = 0;  // (capped, so that it cannot overflow)
+    for (int i = lane; i < a.B; i += 32) {
+        const int64_t length = rows_seq_length<int64_t>(a, rows_seq(a, i), ti) * a.H_kv;
+        sum += min(length, int64_t(1) << 32);
+        mine = int(length);
+    }
+    // A line past ROWS_MAX_LINE is recorded, and no item taken.
     if (__reduce_add_sync(FULL, int(min(sum >> 20, int64_t(1) << 20))) > (ROWS_MAX_LINE >> 20)) {
         if (blockIdx.x == 0 && lane == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
         share = a.min_share;
@@ -229,7 +234,7 @@ __device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane,
     // the sequence that holds it
     int base = 0, seq0 = 0, per = 1, b = -1;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        if (a.B > 32) mine = b0 + lane < a.B ? rows_seq_length(a, rows_seq(a, b0 + lane), ti) * a.H_kv : 0;
+        if (a.B > 32) mine = b0 + lane < a.B ? rows_seq_length<int>(a, rows_seq(a, b0 + lane), ti) * a.H_kv : 0;
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -261,15 +266,15 @@ __device__ __forceinline__ void rows_plan(const RowsTcArgs &a, int ti, int lane,
         // the last block that starts at or before `at`
         if (a.tree_mask) {
             p.qb = (at - p.item0) / (a.item_cost + rows_block_tiles(a, p.s, ti, 0));
-            p.item0 += rows_prefix(a, p.s, ti, p.qb);
+            p.item0 += rows_prefix<int>(a, p.s, ti, p.qb);
         } else if (128 % ti == 0 || ti > 128) {
             int lo = 0, hi = (p.s.n + ti - 1) / ti - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (p.item0 + rows_prefix(a, p.s, ti, mid) <= at) lo = mid; else hi = mid - 1;
+                if (p.item0 + rows_prefix<int>(a, p.s, ti, mid) <= at) lo = mid; else hi = mid - 1;
             }
             p.qb = lo;
-            p.item0 += rows_prefix(a, p.s, ti, lo);
+            p.item0 += rows_prefix<int>(a, p.s, ti, lo);
         } else {
             for (;; ++p.qb) {
                 const int t = a.item_cost + rows_block_tiles(a, p.s, ti, p.qb);
