@@ -1,5 +1,6 @@
 // kvc_rows_simt.cu -- attention of several new tokens per sequence on the CUDA
-// cores: every element type and head width the caches have.
+// cores, for the contiguous caches that the tensor-core kernel does not take:
+// fp32 of every head width, 16-bit types of 32 and 256.
 //
 // A block of four warps takes 16 query rows of one (sequence, KV head) -- row
 // r = i * n + t is head i of the group, token t -- and walks the keys 32 at a
@@ -7,8 +8,10 @@
 // takes four query rows: lane j forms the four scores of key j (fp32 products
 // and sums, K read once for the four rows), the rows' running maximum and sum
 // are kept in the log2 domain, and the probabilities meet V with the lanes on
-// the head's columns.  Bound by the CUDA cores: 16,384 tokens, 32 heads over 8 of
-// 128, in bf16 took 140 ms, 16 TFLOP/s (such caches run on the tensor cores).
+// the head's columns.  Bound by the CUDA cores and by copies that nothing overlaps:
+// 4,096 tokens in fp32, 32 heads over 8 of 128, take 10.4 ms, 13 TFLOP/s; in bf16,
+// 16 heads over 4 of 256, 8.8 ms, 16 TFLOP/s; 16 trees of 16 tokens over 8,192 fp32
+// rows, 32 heads over 8 of 128, 3.8 ms.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -101,32 +104,40 @@ __global__ void __launch_bounds__(WARPS * 32) rows_simt_kernel(const __grid_cons
         const int new_end = a.tree_mask || !one_head ? s.n : int(r_last % s.n) + 1;
         const int end = s.c + new_end;  // keys: cached rows, then new ones
         for (int j0 = 0; j0 < end; j0 += KEYS) {
-            __syncthreads();
-            for (int x = threadIdx.x; x < KEYS * CH; x += blockDim.x) {
-                const int j = x / CH, c16 = x - j * CH, key = j0 + j;
-                uint4 kk = make_uint4(0, 0, 0, 0), vv = kk;
-                if (key < end) {
-                    int64_t row = -1;  // the row's element offset over D
-                    const uint8_t *kp = a.K, *vp = a.V;
-                    if (key >= s.c) {
-                        kp = static_cast<const uint8_t *>(a.k_new), vp = static_cast<const uint8_t *>(a.v_new);
-                        row = rows_offset(a, s, b, a.H_kv, kv, key - s.c, 1);
-                    } else if (a.block_table) {
-                        const int phys = dev::ld(a.block_table + int64_t(b) * a.max_blocks + key / 16);
-                        if (phys < 0 || phys >= a.num_blocks)
-                            dev::record_error(a.err, ERR_DEVICE_INDEX);
-                        else
-                            row = (int64_t(phys) * a.H_kv + kv) * 16 + key % 16;
-                    } else {
-                        row = (int64_t(b) * a.H_kv + kv) * a.max_ctx + key;
-                    }
-                    if (row >= 0) {
-                        kk = dev::ld(reinterpret_cast<const uint4 *>(kp) + row * CH + c16);
-                        vv = dev::ld(reinterpret_cast<const uint4 *>(vp) + row * CH + c16);
-                    }
-                }
+            // vector x of the step's K and V rows
+            auto fetch = [&](int x, uint4 &kk, uint4 &vv) {
+                const int c16 = x % CH, key = j0 + x / CH;
+                kk = vv = make_uint4(0, 0, 0, 0);
+                if (key >= end) return;
+                const bool cached = key < s.c;
+                const uint8_t *kp = cached ? a.K : static_cast<const uint8_t *>(a.k_new);
+                const uint8_t *vp = cached ? a.V : static_cast<const uint8_t *>(a.v_new);
+                // the row's element offset over D
+                const int64_t row = cached ? (int64_t(b) * a.H_kv + kv) * a.max_ctx + key
+                                           : rows_offset(a, s, b, a.H_kv, kv, key - s.c, 1);
+                kk = dev::ld(reinterpret_cast<const uint4 *>(kp) + row * CH + c16);
+                vv = dev::ld(reinterpret_cast<const uint4 *>(vp) + row * CH + c16);
+            };
+            auto store = [&](int x, const uint4 &kk, const uint4 &vv) {
+                const int j = x / CH, c16 = x % CH;
                 ks[j * (CH + 1) + c16] = kk;
                 *reinterpret_cast<uint4 *>(vs + j * D + c16 * VEC) = vv;
+            };
+            constexpr int PER = KEYS * CH / (WARPS * 32);  // vectors of K, and of V, per thread
+            if constexpr (PER <= 2) {  // (few enough to be on their way while other warps end the step before)
+                uint4 kk[PER], vv[PER];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) fetch(threadIdx.x + i * WARPS * 32, kk[i], vv[i]);
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < PER; ++i) store(threadIdx.x + i * WARPS * 32, kk[i], vv[i]);
+            } else {
+                __syncthreads();
+                for (int x = threadIdx.x; x < KEYS * CH; x += blockDim.x) {
+                    uint4 kk, vv;
+                    fetch(x, kk, vv);
+                    store(x, kk, vv);
+                }
             }
             __syncthreads();
             float sc[RW];
@@ -194,11 +205,13 @@ cudaError_t launch_type(const RowsArgs &a, int D, int parts, cudaStream_t s) {
     const dim3 grid(unsigned(int64_t(a.B) * a.H_kv * parts));
     switch (D) {
         case 32: return launch_pdl(rows_simt_kernel<T, 32>, grid, dim3(WARPS * 32), 0, s, a, parts);
-        case 64: return launch_pdl(rows_simt_kernel<T, 64>, grid, dim3(WARPS * 32), 0, s, a, parts);
-        case 128: return launch_pdl(rows_simt_kernel<T, 128>, grid, dim3(WARPS * 32), 0, s, a, parts);
         case 256: return launch_pdl(rows_simt_kernel<T, 256>, grid, dim3(WARPS * 32), 0, s, a, parts);
-        default: return cudaErrorInvalidValue;
     }
+    if constexpr (sizeof(T) == 4) {
+        if (D == 64) return launch_pdl(rows_simt_kernel<T, 64>, grid, dim3(WARPS * 32), 0, s, a, parts);
+        if (D == 128) return launch_pdl(rows_simt_kernel<T, 128>, grid, dim3(WARPS * 32), 0, s, a, parts);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
