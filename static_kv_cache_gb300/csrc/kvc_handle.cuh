@@ -45,6 +45,12 @@ namespace kvc {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Is the handle's device the calling thread's?
+inline bool device_current(const kvc_cache *h) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
 inline uint64_t layer_scale_bytes(const kvc_cache *h) {
     const kvc_config &c = h->cfg;
     return uint64_t(c.batch) * c.n_kv_heads * uint64_t(c.max_context) * 4;

@@ -141,7 +141,9 @@ __device__ __forceinline__ bool wants(const PagesArgs &a, const int32_t *first, 
 // sequence, are one list of places; a prefix sum over the places that want a
 // page gives each its number in the order of hand-out, another one over the
 // counts finds the lowest free blocks.  Only if those suffice is anything changed.
-// Bound by the latency of its passes: 10 us for 64 sequences.
+// Bound by the latency of its passes: 10 us for 64 sequences.  `wants` walks the
+// earlier sequences of a shared page one by one: beams of one parent that all
+// write their shared page take 0.1 ms at 1,024 sequences and 6.8 ms at 8,192.
 __global__ void __launch_bounds__(1024) reserve_kernel(const __grid_constant__ PagesArgs a, const Reserve r) {
     extern __shared__ int32_t dyn[];
     int32_t *first = dyn, *offset = dyn + a.B;  // [B] first logical block, [B + 1] first place
@@ -358,11 +360,6 @@ Workspace pages_workspace(const kvc_config *c, int32_t num_blocks) {
     w.where = w.list + blocks;
     w.total = w.where + blocks;
     return w;
-}
-
-bool device_current(const kvc_cache *h) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
 // What every call fills in: the pools, and the shape of the table.

@@ -8,10 +8,7 @@
 
 namespace {
 
-bool device_current(const kvc_cache *h) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
-}
+using kvc::device_current;
 
 // What both attentions fill in alike.
 kvc::RowsArgs rows_args(const kvc_cache *h, int32_t layer) {
