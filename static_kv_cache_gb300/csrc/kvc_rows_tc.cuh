@@ -51,10 +51,10 @@
 // only the rows that see them: such elements are zeroed, and the epilogue of
 // the rows that see them adds them back.
 //
-// Measured (bf16, 32 heads over 8, d_h 128): 16,384 tokens 1.47 ms, 1.49 PFLOP/s,
+// Measured (bf16, 32 heads over 8, d_h 128): 16,384 tokens 1.47 ms, 1.50 PFLOP/s,
 // bound by the hand-overs between a stream's MMAs and its softmax; 8 prompts of
-// 64-2,048 tokens over up to 1,500 rows in pages 226 us, the same and about 5 us
-// at each item's ends; 16 trees of 32 tokens over 1,024-8,192 rows in pages 67 us,
+// 64-2,048 tokens over up to 1,500 rows in pages 222 us, the same and about 5 us
+// at each item's ends; 16 trees of 32 tokens over 1,024-8,192 rows in pages 68 us,
 // 5.0 TB/s, bound by the copies and the start and end of the launch.
 //
 // Every wait is bounded; a timeout records KVC_ERR_TIMEOUT, every role leaves
