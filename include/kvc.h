@@ -247,7 +247,8 @@ void kvc_free(kvc_cache *h);
 /* Override the number of context splits (CTAs) of kvc_decode_attn (and
  * kvc_packed_attn): 0 restores the automatic choice, otherwise 1..1024 (on a
  * KVC_E4M3 handle more than 160 count as 160).  Results agree across split
- * counts up to fp32 rounding. */
+ * counts up to fp32 rounding (KVC_E4M3: up to that of the probabilities, as
+ * kvc_packed_attn has it). */
 kvc_status kvc_set_num_splits(kvc_cache *h, int32_t n);
 
 /* Limit, in nanoseconds of GPU wall time, of one wait inside the decode
@@ -581,10 +582,11 @@ kvc_status kvc_append_rope(kvc_cache *h, int32_t layer, const kvc_rope *rope, co
  * sequence are left unwritten.
  * Arithmetic: where sequences have up to 64 query rows per KV head on average, the
  * codes are the tensor cores' operands; a query element is the sum of three e4m3 values
- * (off by 2^-12 of itself or 2^-17 of its row's largest), a probability is rounded to
- * fp16 and split likewise.  Otherwise codes are taken as fp16 (exact), query elements
- * too, scaled by a power of two (off by 2^-39 of their row's largest at most), and
- * probabilities are rounded to fp16.  The softmax's sum takes probabilities as they
+ * (off by 2^-12 of itself or 2^-17 of its row's largest).  Otherwise codes are taken as
+ * fp16 (exact), query elements too, scaled by a power of two (off by 2^-39 of their row's
+ * largest at most).  Either way a probability, times its block's scale of V, is rounded to
+ * fp16: off by 2^-11 of itself or by 2^-29 of the largest such product that its row has
+ * met, whichever is more.  The softmax's sum takes probabilities as they
  * were; fp32 products and sums, one round-to-nearest-even at the end.
  * Limit of one call: 2^30 steps, where a block of floor(r / g) tokens of a sequence
  * (r: 64, or fewer where sequences have fewer query rows per KV head on average; 256

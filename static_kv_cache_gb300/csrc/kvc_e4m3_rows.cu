@@ -4,7 +4,7 @@
 // The kernel of kvc_e4m3_tc.cuh has keys on M, so that few query rows cost little.
 // With 128 query rows and more that order pays for each row what this one pays for
 // 128: a row's scores lie in one thread, so that maximum and sum need no other, and a
-// probability is one fp16 value instead of three of 8 bits.
+// probability is one fp16 value instead of four of 8 bits.
 //
 // A tile of the line (kvc_e4m3_tc.cuh) is 128 keys of one KV head, a segment up to
 // 2 TB tokens (TB = 128 / g) of one (sequence, KV head) as two query tiles of 128 rows,

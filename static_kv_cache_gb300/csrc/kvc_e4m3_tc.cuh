@@ -14,10 +14,13 @@
 // sum of three of them, each what the ones before leave (off by 2^-12, or by 2^-17 of
 // the row's largest): three columns, added up as they are read, or, where a tile has
 // many query rows, three products into one column.  A probability is
-// rounded to fp16 (2^-11; the sum takes it as it is) and split in three as well, each 16
-// times what the ones before leave (off by 2^-18 at least): three columns, added up at a
-// piece's end with the factors 1, 1/16 and 1/256.  The
-// tensor cores have the time: they read A for as long as N = 64 takes them.
+// rounded to fp16 (2^-11; the sum takes it as it is) and split in four, each 32 times what
+// the ones before leave, which is exact: four columns, added up at a piece's end with the
+// factors 1, 2^-5, 2^-10 and 2^-15.  With three, 16 times what is left, whatever was 2^-18
+// of a row's first maximum was lost, and with it, beside one key with 97 % of the weight, much of
+// what 16,384 others add up to (the fourth costs 4 %: 32 heads on one KV head 20.9 -> 21.8
+// us, drafts 27.9 -> 29.1).  The tensor cores have the time: they read A for as long as
+// N = 64 takes them.
 //
 // A tile is 128 rows: the blocks of 16 rows of NH KV heads that lie one behind
 // another in the pool, of 8 / NH pages.  One box brings a page's NH heads (NH * 2
@@ -33,14 +36,18 @@
 // thread has one key.  P' is MN-major, so that a thread's probabilities, of all its
 // head's query rows, are neighbouring bytes.  A pair (head, query row) has one
 // reference mo, of the scores with the values' scale in them: P' = 2^(s + log2 vs -
-// mo) stays within e4m3's range (up to 2^8, down to 2^-18 with three of them)
-// whatever the blocks' scales, and P' / vs sums up to what the output is divided by.
+// mo) stays within the range of the four values (up to 2^8, down to 2^-24, fp16's
+// smallest) whatever the blocks' scales, and P' / vs sums up to what the output is divided
+// by.
 // (Scales of values below 2^-90, zeros among them, count as that in a reference, so
 // that no sum overflows; below 2^-40 the sum has an exponential of its own, as P' may be flushed
 // to zero beside values of common size; and where references differ, sums take the
 // factor in two steps, as one may be below what fp32 has.)  The
 // references are raised, and the maxima taken at all, only where a P' would pass
-// 2^8: else a tile costs the group one barrier that carries the question.
+// 2^8: else a tile costs the group one barrier that carries the question.  A reference is
+// set so that the row's largest P' is 2^4: what fp16 rounds away of one is 2^-29 of that at
+// most, and a later score has four bits to go (at 2^0, 2^2, 2^3, 2^4, 2^6: 32 heads on one KV
+// head 21.8, 21.8, 22.3, 22.5, 24.3 us; a batch 33.3, 33.7, 33.6, 34.0, 37.1).
 //
 // The line of all tiles (sequence after sequence, head group, query rows) is cut
 // into equal shares; a cut segment's pieces go to the workspace as partial results,
@@ -65,7 +72,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int TILE = 128, TILE_BYTES = TILE * E4M3_D, STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int MAX_STAGES = 6;
 constexpr uint32_t TMEM_COLS = 512, S_COL = 0, S_NEXT = 128, O_COL = 256, O_NEXT = 128;  // (a group's)
-constexpr float RESCALE_LOG2 = 8.f, SMALL_LOG2 = -40.f;
+constexpr float RESCALE_LOG2 = 8.f, START_LOG2 = 4.f, SMALL_LOG2 = -40.f;
 constexpr int64_t MAX_LINE = 1 << 30;  // tiles of a call (places are 32-bit numbers)
 constexpr int GROUPS = 2;
 // Softmax warps: two groups of 4, or of 8 where a tile has 16 or 32 query rows per
@@ -474,17 +481,19 @@ __device__ __forceinline__ void join(const E4m3TcArgs &a, int64_t out_row, int f
     }
 }
 
-// An fp16 pair's three e4m3 values each, the next 16 times what the ones before
-// leave (exact: fp16 has 11 bits, the three take 12).
-__device__ __forceinline__ void split3(uint32_t h, uint32_t (&c)[3]) {
-    const __half2 minus = __float2half2_rn(-16.f), times = __float2half2_rn(16.f);
+// An fp16 pair's four e4m3 values each, the next 32 times what the ones before leave:
+// exact up to 2^8.  A value leaves at most 2^-4 of what it is of, 8 of 2^8, so the next
+// is 2^8 at most too; three take 12 bits of fp16's 11, and the fourth's last step, 2^-9 *
+// 2^-15, is fp16's smallest number.
+__device__ __forceinline__ void split4(uint32_t h, uint32_t (&c)[4]) {
+    const __half2 minus = __float2half2_rn(-32.f), times = __float2half2_rn(32.f);
     __half2 x = *reinterpret_cast<const __half2 *>(&h);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 4; ++k) {
         uint16_t r;
         asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
         c[k] = r;
-        if (k < 2) {
+        if (k < 3) {
             const uint32_t back = dev::e4m3x2_to_f16x2(c[k]);
             x = __hfma2(*reinterpret_cast<const __half2 *>(&back), minus, __hmul2(x, times));
         }
@@ -875,13 +884,13 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
                         }
                         // (keys that a row sees come before those it does not: one that sees
                         // none in its first tile sees none later)
-                        const float delta = i == first ? (top == -INFINITY ? 0.f : top) : fmaxf(top, 0.f);
+                        const float delta = i == first ? (top == -INFINITY ? 0.f : top - START_LOG2) : fmaxf(top - START_LOG2, 0.f);
                         corr = ex2(-0.5f * delta);
                         mo = i == first ? delta : mo + delta;
                         sm.neg[g][lane] = -mo;
                         sm.delta[g][lane] = delta;
-                        sm.corr[g][lane] = corr;
                     }
+                    sm.corr[g][lane] = corr;
                     __syncwarp();
                     {
                         float y[RW];
@@ -897,17 +906,20 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
                         // O of the tiles before, at the new references
                         tc::fence_after();
                         const uint32_t at = tmem + lanes + O_COL + uint32_t(g) * O_NEXT;
-                        for (int c0 = 8 * part; c0 < 3 * ps; c0 += 8 * C::SPLIT) {
-                            uint32_t o[8];
-                            tmem_ld<8>(at + uint32_t(c0), o);
+                        for (int c0 = 16 * part; c0 < 4 * ps; c0 += 16 * C::SPLIT) {
+                            uint32_t o[16];
+                            tmem_ld<16>(at + uint32_t(c0), o);
                             tc::tmem_ld_wait();
-                            reg_fence<8>(o);
+                            reg_fence<16>(o);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int pair = (c0 + k) & (ps - 1);
-                                if (pair < pairs) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.corr[g][pair] * sm.corr[g][pair]);
+                            for (int k = 0; k < 16; k += 4) {
+                                float y[4];
+                                load_row<4>(sm.corr[g] + ((c0 + k) & (ps - 1)), y);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[k + e] = __float_as_uint(__uint_as_float(o[k + e]) * y[e] * y[e]);
                             }
                             tmem_st8(at + uint32_t(c0), o);
+                            tmem_st8(at + uint32_t(c0) + 8, o + 8);
                         }
                         tc::tmem_st_wait();
                     }
@@ -925,7 +937,7 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
                 constexpr int W = RW < 16 ? RW : 16;  // bytes of a store
 #pragma unroll
                 for (int q0 = 0; q0 < RW; q0 += W) {
-                    uint32_t c[3][W < 4 ? 1 : W / 4];
+                    uint32_t c[4][W < 4 ? 1 : W / 4];
 #pragma unroll
                     for (int e = 0; e < W; e += 2) {
                         float2 f = make_float2(ex2(v[q0 + e]), 0.f);
@@ -937,13 +949,13 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
                             sum[0] = fmaf(f.x, per, sum[0]);
                         }
                         const __half2 h = __floats2half2_rn(f.x, f.y);
-                        uint32_t two[3];
-                        split3(*reinterpret_cast<const uint32_t *>(&h), two);
+                        uint32_t two[4];
+                        split4(*reinterpret_cast<const uint32_t *>(&h), two);
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) c[k][e / 4] = e % 4 ? __byte_perm(c[k][e / 4], two[k], 0x5410) : two[k];
+                        for (int k = 0; k < 4; ++k) c[k][e / 4] = e % 4 ? __byte_perm(c[k][e / 4], two[k], 0x5410) : two[k];
                     }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const uint32_t n = uint32_t(k * ps + r0 + q0), to = p_row + (((n >> 4) ^ p_swz) << 4) + (n & 15);
                         if constexpr (W == 16)
                             dev::st_shared_v4(to, make_uint4(c[k][0], c[k][1], c[k][2], c[k][3]));
@@ -1015,17 +1027,19 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
 #pragma unroll
                 for (int x = 0; x < GROUPS; ++x) {
                     if (WIDE && x != g) continue;
-                    uint32_t o[3][8];
+                    uint32_t o[4][8];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) tmem_ld<8>(tmem + lanes + O_COL + uint32_t(x) * O_NEXT + uint32_t(k * ps + c0), o[k]);
+                    for (int k = 0; k < 4; ++k) tmem_ld<8>(tmem + lanes + O_COL + uint32_t(x) * O_NEXT + uint32_t(k * ps + c0), o[k]);
                     tc::tmem_ld_wait();
                     const bool there = WIDE || tiles > 1 || ((t0 - 1) & 1) == x;  // (a group without a tile has no accumulator)
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) reg_fence<8>(o[k]);
+                    for (int k = 0; k < 4; ++k) reg_fence<8>(o[k]);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float z = fmaf(fmaf(__uint_as_float(o[2][k]), 0.0625f, __uint_as_float(o[1][k])), 0.0625f, __uint_as_float(o[0][k])) *
-                                        __shfl_sync(FULL, fo[x], c0 + k);
+                        float z = __uint_as_float(o[3][k]);
+#pragma unroll
+                        for (int v = 2; v >= 0; --v) z = fmaf(z, 0x1p-5f, __uint_as_float(o[v][k]));
+                        z *= __shfl_sync(FULL, fo[x], c0 + k);
                         y[k] += there ? z : 0.f;
                     }
                 }
