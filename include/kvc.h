@@ -306,7 +306,9 @@ kvc_status kvc_append(kvc_cache *h, int32_t layer, const void *k_new,
  *                   unwritten) and KVC_ERR_DEVICE_INDEX is recorded.
  *   max_valid_hint  host; 0, or an upper bound on valid_len used only to size
  *                   the launch without a device-to-host read.
- *   out             device, [B, H, d_h]
+ *   out             device, [B, H, d_h]; on a KVC_E4M3 handle 16-byte aligned and
+ *                   apart from q (KVC_ERR_INVALID, also where the handle's device
+ *                   is not current; KVC_ERR_UNSUPPORTED: B * n_heads past 2^31 - 1)
  * Host errors: KVC_ERR_INVALID, KVC_ERR_ALIGNMENT, KVC_ERR_CUDA. */
 kvc_status kvc_decode_attn(kvc_cache *h, int32_t layer, const void *q,
                            const int32_t *valid_len, int32_t max_valid_hint,
@@ -571,7 +573,7 @@ kvc_status kvc_append_rope(kvc_cache *h, int32_t layer, const kvc_rope *rope, co
  * prompt's chunk.  Rows that a token does not see never reach its output, whatever
  * they hold (but see KVC_E4M3 on blocks with a NaN scale).
  *   q, out       device, [total, H, d_h] in the handle's row type, 16-byte aligned;
- *                not the same
+ *                they must not overlap
  *   cu_seqlens, cache_index, total   as for kvc_append_rope
  *   max_rows_hint  host; 0, or an upper bound on cache_index[b] plus b's tokens,
  *                used only to size the launch

@@ -631,10 +631,8 @@ kvc_status kvc_decode_step(kvc_cache *h, int32_t layer, const void *q, const voi
         return KVC_ERR_INVALID;
     if (max_valid_hint < 0 || max_valid_hint > h->cfg.max_context) return KVC_ERR_INVALID;
     if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new)) return KVC_ERR_ALIGNMENT;
-    if (h->cfg.dtype == KVC_E4M3) {  // (the append may have to rewrite a block that the attention reads: two launches)
-        const kvc_status st = kvc::e4m3_append(h, layer, k_new, v_new, valid_len, -1, 1, stream);
-        return st != KVC_OK ? st : kvc::e4m3_decode(h, layer, q, valid_len, max_valid_hint, out, stream);
-    }
+    // (the append may have to rewrite a block that the attention reads: two launches)
+    if (h->cfg.dtype == KVC_E4M3) return kvc::e4m3_step(h, layer, q, k_new, v_new, valid_len, max_valid_hint, out, stream);
     // one launch: every other decode kernel appends (an int8 cache: quantises) the
     // step's new rows as it streams
     return launch_decode(h, layer, q, valid_len, max_valid_hint, out, stream, k_new, v_new);

@@ -66,12 +66,21 @@ bool encode_pools(kvc_cache *h) {
     return true;
 }
 
+// What an attention call refuses, looked at before anything is enqueued.
+kvc_status refusal(const kvc_cache *h, const void *q, const void *out, int32_t total) {
+    if (!device_current(h)) return KVC_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(out)) return KVC_ERR_ALIGNMENT;  // (pieces are joined 8 bytes at a time)
+    const int64_t rows = int64_t(total) * h->cfg.n_heads;
+    if (rows > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
+    // (a row's pieces are several CTAs', which read its queries)
+    const uintptr_t bytes = uintptr_t(rows) * kvc::E4M3_D * row_bytes_of(h), a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(out);
+    return (a < b ? b - a : a - b) < bytes ? KVC_ERR_INVALID : KVC_OK;
+}
+
 kvc_status attend(const kvc_cache *h, int32_t layer, const void *q, const int32_t *cu_seqlens, const int32_t *cache_index,
                   int index_offset, int32_t total, int32_t hint, void *out, void *stream) {
     const kvc_config &c = h->cfg;
     const uint64_t slab = kvc::layer_slab_bytes(h), ss = kvc::layer_scale_bytes(h);
-    if (out == q) return KVC_ERR_INVALID;  // (a row's pieces are several CTAs', which read its queries)
-    if (int64_t(total) * c.n_heads > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     kvc::E4m3TcArgs a{};
     a.K = h->k_base + slab * layer;
     a.V = h->v_base + slab * layer;
@@ -179,8 +188,15 @@ kvc_status kvc::e4m3_append_packed(const kvc_cache *h, int32_t layer, const void
 
 kvc_status kvc::e4m3_decode(const kvc_cache *h, int32_t layer, const void *q, const int32_t *valid_len, int32_t max_valid_hint,
                             void *out, void *stream) {
-    if (!device_current(h)) return KVC_ERR_INVALID;
-    return attend(h, layer, q, nullptr, valid_len, -1, h->cfg.batch, max_valid_hint, out, stream);
+    const kvc_status st = refusal(h, q, out, h->cfg.batch);
+    return st != KVC_OK ? st : attend(h, layer, q, nullptr, valid_len, -1, h->cfg.batch, max_valid_hint, out, stream);
+}
+
+kvc_status kvc::e4m3_step(const kvc_cache *h, int32_t layer, const void *q, const void *k_new, const void *v_new,
+                          const int32_t *valid_len, int32_t max_valid_hint, void *out, void *stream) {
+    kvc_status st = refusal(h, q, out, h->cfg.batch);
+    if (st == KVC_OK) st = e4m3_append(h, layer, k_new, v_new, valid_len, -1, 1, stream);
+    return st != KVC_OK ? st : attend(h, layer, q, nullptr, valid_len, -1, h->cfg.batch, max_valid_hint, out, stream);
 }
 
 extern "C" {
@@ -290,9 +306,9 @@ kvc_status kvc_packed_attn(kvc_cache *h, int32_t layer, const void *q, const int
     if (h->cfg.dtype != KVC_E4M3) return KVC_ERR_UNSUPPORTED;
     if (!cu_seqlens && total != h->cfg.batch) return KVC_ERR_INVALID;
     if (total == 0) return KVC_OK;
-    if (!q || !out || !device_current(h)) return KVC_ERR_INVALID;
-    if (!aligned16(q) || !aligned16(out)) return KVC_ERR_ALIGNMENT;
-    return attend(h, layer, q, cu_seqlens, cache_index, 0, total, max_rows_hint, out, stream);
+    if (!q || !out) return KVC_ERR_INVALID;
+    const kvc_status st = refusal(h, q, out, total);
+    return st != KVC_OK ? st : attend(h, layer, q, cu_seqlens, cache_index, 0, total, max_rows_hint, out, stream);
 }
 
 }  // extern "C"

@@ -73,6 +73,8 @@ kvc_status e4m3_append_packed(const kvc_cache *h, int32_t layer, const void *k, 
                               const int32_t *cache_index, int32_t total, void *stream);
 kvc_status e4m3_decode(const kvc_cache *h, int32_t layer, const void *q, const int32_t *valid_len, int32_t max_valid_hint,
                        void *out, void *stream);
+kvc_status e4m3_step(const kvc_cache *h, int32_t layer, const void *q, const void *k_new, const void *v_new,
+                     const int32_t *valid_len, int32_t max_valid_hint, void *out, void *stream);
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
