@@ -98,8 +98,8 @@ typedef enum {
  * where the block's scale is, if the call stores the block's first row, the
  * smallest power of two with absmax <= 448 * scale over the block's new rows
  * (not below 2^-126; 0 for zeros); otherwise the scale it had, where the new rows
- * fit it, or else that power of two, and the codes of the rows before become
- * e4m3(code * (old scale * (1 / scale))).  A new row with an infinity or NaN makes
+ * fit it and it is 0 or 2^-126 at least, or else that power of two (2^-126 at least),
+ * and the codes of the rows before become e4m3(code * (old scale * (1 / scale))).  A new row with an infinity or NaN makes
  * the block's scale NaN: its rows read as NaN until its first row is stored again.
  * A cache filled by other means may hold any finite scales >= 0, and no NaN codes
  * (0x7f, 0xff) in live rows.  Scales of values below 2^-90 but 0 may be taken as 2^-90;

@@ -312,7 +312,10 @@ __device__ __forceinline__ void page_rows(const RopeArgs &a, int b, int lo, int 
     const uint32_t bits = __reduce_max_sync(FULL, __float_as_uint(most) & 0x7fffffffu);  // (infinities and NaN are above all)
     const bool odd = bits >= 0x7f800000u || old != old;
     const float top = __uint_as_float(bits);
-    const float scale = odd ? __int_as_float(0x7fffffff) : top <= 448.f * old ? old : e4m3_scale(top);
+    // (a scale below 2^-126, which only a cache filled by other means has, is not kept: its
+    // reciprocal may be infinite, and a zero's code then NaN)
+    const bool fits = top <= 448.f * old && (old == 0.f || old >= 0x1p-126f);
+    const float scale = odd ? __int_as_float(0x7fffffff) : fits ? old : fmaxf(e4m3_scale(top), old > 0.f ? 0x1p-126f : 0.f);
     const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
     if (s0 > 0 && !odd && scale != old) {
         // the rows before, at the new scale
