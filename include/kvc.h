@@ -262,7 +262,9 @@ kvc_status kvc_set_num_splits(kvc_cache *h, int32_t n);
  * memory, and the drain of copies in flight before a block exits) keeps the
  * 1 s default, so no block ever exits with a copy still landing.  A short
  * limit is meant for diagnostics: under load the other splits may
- * legitimately take longer than it. */
+ * legitimately take longer than it.  On a KVC_E4M3 handle, whose kernels wait
+ * for no other block, it is the limit of each wait of an attention call for
+ * copies, products and other warps; the drain keeps 1 s there too. */
 kvc_status kvc_set_wait_timeout_ns(kvc_cache *h, uint64_t ns);
 
 /* ---- the decode step ------------------------------------------------------ */
@@ -742,7 +744,7 @@ kvc_status kvc_static_get_error(void *stream);
 /* Synchronise the stream, then read and clear the device error word.
  * Returns KVC_OK if no kernel recorded an error since the last call,
  * otherwise the first recorded code (KVC_ERR_DEVICE_INDEX or
- * KVC_ERR_TIMEOUT).  After KVC_ERR_TIMEOUT the split counters are reset too.
+ * KVC_ERR_TIMEOUT).  After an error the split counters are reset too.
  * KVC_ERR_CUDA if the synchronisation or the copy fails. */
 kvc_status kvc_get_error(kvc_cache *h, void *stream);
 

@@ -690,11 +690,10 @@ kvc_status kvc_get_error(kvc_cache *h, void *stream) {
         return KVC_ERR_CUDA;
     if (word != 0) {
         if (cudaMemset(h->ws, 0, sizeof word) != cudaSuccess) return KVC_ERR_CUDA;
-        if (word == KVC_ERR_TIMEOUT) {
-            // an aborted launch can leave counters and publish flags set
-            const uint64_t n = h->wl.part_ml - h->wl.tickets;
-            if (cudaMemset(h->ws + h->wl.tickets, 0, n) != cudaSuccess) return KVC_ERR_CUDA;
-        }
+        // an aborted launch can leave counters and publish flags set (one whose error was
+        // not the first, too)
+        const uint64_t n = h->wl.part_ml - h->wl.tickets;
+        if (cudaMemset(h->ws + h->wl.tickets, 0, n) != cudaSuccess) return KVC_ERR_CUDA;
         if (cudaDeviceSynchronize() != cudaSuccess) return KVC_ERR_CUDA;
     }
     return static_cast<kvc_status>(word);

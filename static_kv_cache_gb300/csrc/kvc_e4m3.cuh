@@ -69,7 +69,7 @@ struct E4m3TcArgs : E4m3Args {
     int32_t n_stages, min_share; // tiles of a CTA's share, at least
     int32_t layer_block;         // first block of the layer in the maps
     int32_t read_once;           // no two segments read the same rows
-    unsigned long long timeout_ns;
+    unsigned long long timeout_ns;  // limit of a wait, but for those before the block leaves
     CUtensorMap tm_k, tm_v;      // (128, 16 rows, H_kv, L * num_blocks), boxes of nh heads of a block
 };
 

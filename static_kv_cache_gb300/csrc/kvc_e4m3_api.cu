@@ -108,7 +108,7 @@ kvc_status attend(const kvc_cache *h, int32_t layer, const void *q, const int32_
     a.part_ml = reinterpret_cast<float2 *>(h->ws + w.part_ml);
     a.part_acc = reinterpret_cast<float *>(h->ws + w.part_acc);
     a.layer_block = layer * h->num_blocks;
-    a.timeout_ns = kvc::WAIT_TIMEOUT_NS;
+    a.timeout_ns = h->flag_timeout_ns;
     // Query rows of a tile: those of the tokens that a sequence has on average, up to 64.
     const int64_t tokens = cu_seqlens ? (int64_t(total) + c.batch - 1) / c.batch : 1;
     int rows = 1;

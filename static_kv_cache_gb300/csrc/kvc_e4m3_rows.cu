@@ -126,6 +126,9 @@ __device__ __forceinline__ void store32(const E4m3TcArgs &a, int row, int q, con
     }
 }
 
+// SHORT: for limits below those for which rows_wait suspends a warp (as an operand of the
+// waits that time costs 2 % of a call).
+template <bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1) e4m3_rows_kernel(const __grid_constant__ E4m3TcArgs a) {
     constexpr uint32_t IDESC_S = tc::idesc_f16_f32acc(false, 128, 128, false, false), IDESC_O = tc::idesc_f16_f32acc(false, 128, 128, false, true);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -175,7 +178,9 @@ __global__ void __launch_bounds__(THREADS, 1) e4m3_rows_kernel(const __grid_cons
 
     Walker walk;
     const bool any = walk.init(a, sm.plan, warp, THREADS / 32, lane);
-    const auto wait = [&](uint32_t b, uint32_t parity) { return rows_wait(b, parity, flags, a.timeout_ns); };
+    const auto wait = [&](uint32_t b, uint32_t parity) {
+        return SHORT ? dev::mbar_wait_bounded(b, parity, flags, a.timeout_ns) : rows_wait(b, parity, flags, a.timeout_ns);
+    };
     const auto fail = [&] {
         if (lane == 0) {
             if (!flags[0]) dev::record_error(a.err, ERR_TIMEOUT);
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) e4m3_rows_kernel(const __grid_cons
             // every MMA is done before tensor memory is freed
             tc::commit(bar(sm.mma_done));
             const volatile int never = 0;
-            rows_wait(bar(sm.mma_done), 0, &never, a.timeout_ns);
+            rows_wait(bar(sm.mma_done), 0, &never, WAIT_TIMEOUT_NS);
         }
         __syncwarp();
     } else {
@@ -653,16 +658,19 @@ __global__ void __launch_bounds__(THREADS, 1) e4m3_rows_kernel(const __grid_cons
     if (warp == 8 && lane == 0 && flags[0]) {
         // after an abort, the copies that may still land
         const volatile int never = 0;
-        for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i) rows_wait(bar(sm.raw[i % NS]), (i / NS) & 1, &never, a.timeout_ns);
+        for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i) rows_wait(bar(sm.raw[i % NS]), (i / NS) & 1, &never, WAIT_TIMEOUT_NS);
     }
 }
 
 }  // namespace
 
-cudaError_t e4m3_rows_set_max_smem() { return cudaFuncSetAttribute(e4m3_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); }
+cudaError_t e4m3_rows_set_max_smem() {
+    const cudaError_t e = cudaFuncSetAttribute(e4m3_rows_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(e4m3_rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+}
 
 cudaError_t launch_e4m3_rows(const E4m3TcArgs &a, int grid, cudaStream_t s) {
-    return launch_pdl(e4m3_rows_kernel, dim3(grid), dim3(THREADS), SMEM, s, a);
+    return launch_pdl(a.timeout_ns < WAIT_TIMEOUT_NS / 100 ? e4m3_rows_kernel<true> : e4m3_rows_kernel<false>, dim3(grid), dim3(THREADS), SMEM, s, a);
 }
 
 }  // namespace kvc

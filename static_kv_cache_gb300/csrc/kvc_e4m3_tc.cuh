@@ -56,7 +56,8 @@
 //
 // Warps: 0 copies, 1 issues S, 2 issues O, the others softmax and epilogue.  After a wait
 // that ran out (KVC_ERR_TIMEOUT) the softmax warps go through the rest of their
-// tiles without waiting, so that all meet at the same barriers.
+// tiles without waiting, so that all meet at the same barriers.  The waits for copies and
+// products in flight before the block leaves keep their limit, whatever the handle's is.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
             // every MMA issued here has completed before tensor memory is freed
             tc::commit(bar(sm.mma_done));
             const volatile int never = 0;
-            dev::mbar_wait_bounded(bar(sm.mma_done), 0, &never, a.timeout_ns);
+            dev::mbar_wait_bounded(bar(sm.mma_done), 0, &never, WAIT_TIMEOUT_NS);
         }
         __syncwarp();
     } else if (warp >= SOFT0) {
@@ -1094,7 +1095,7 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
         // after an abort, the copies that may still land
         const volatile int never = 0;
         for (int i = issued > ns ? issued - ns : 0; i < issued; ++i)
-            dev::mbar_wait_bounded(bar(sm.full[i % ns]), uint32_t(i / ns) & 1, &never, a.timeout_ns);
+            dev::mbar_wait_bounded(bar(sm.full[i % ns]), uint32_t(i / ns) & 1, &never, WAIT_TIMEOUT_NS);
     }
 }
 

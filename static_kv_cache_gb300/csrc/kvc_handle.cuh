@@ -19,7 +19,7 @@ struct kvc_cache {
     int row_dtype;           // kvc_dtype of q, new rows and outputs: the cache's own, but for 8-bit caches
     int group;               // n_heads / n_kv_heads
     int num_splits;          // 0: automatic
-    uint64_t flag_timeout_ns;  // limit of the split combine's wait for the other splits
+    uint64_t flag_timeout_ns;  // limit of the split combine's wait for the other splits; e4m3: of every wait within a block
     uint8_t *k_base;
     uint8_t *v_base;
     uint8_t *k_scale;        // int8 caches: per-row fp32 scales [L, B, H_kv, T_max]; e4m3: [L, num_blocks, H_kv]; else null
