@@ -100,7 +100,12 @@ typedef enum {
  * (not below 2^-126; 0 for zeros); otherwise the scale it had, where the new rows
  * fit it and it is 0 or 2^-126 at least, or else that power of two (2^-126 at least),
  * and the codes of the rows before become e4m3(code * (old scale * (1 / scale))).  A new row with an infinity or NaN makes
- * the block's scale NaN: its rows read as NaN until its first row is stored again.
+ * the block's scale NaN: its rows read as NaN until that row, or one before it, is
+ * stored again.  The rows before it are kept in that NaN's last bits, at a scale that is a
+ * power of two (what the rule gives, or the next one up), and are there again then; it
+ * and the rows behind it in the block are lost.  (Another NaN in a scale's place: until
+ * the block's first row is stored again.)  A call's new rows of such a block are stored
+ * one by one.  A scale does not shrink before the block's first row is stored again.
  * A cache filled by other means may hold any finite scales >= 0, and no NaN codes
  * (0x7f, 0xff) in live rows.  Scales of values below 2^-90 but 0 may be taken as 2^-90;
  * beside scales of values above 2^60, rows whose scale is more than 2^100 smaller may

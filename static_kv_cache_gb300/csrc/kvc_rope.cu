@@ -266,12 +266,102 @@ __device__ __forceinline__ float e4m3_scale(float top) {
     return __uint_as_float(uint32_t(max(e, 1)) << 23);
 }
 
-// New rows [i0, i0 + n) of sequence b, all of one block, of KV head j of K or V.
+// The codes of a block's first rows, times f.
+__device__ __forceinline__ void rescale_rows(uint8_t *block, int rows, float f, int lane) {
+            for (int x16 = lane; x16 < rows * (E4M3_D / 16); x16 += 32) {
+                uint4 v = dev::ld(reinterpret_cast<const uint4 *>(block) + x16);
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    #pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t l2 = dev::e4m3x2_to_f16x2(w[t] & 0xffffu), h2 = dev::e4m3x2_to_f16x2(w[t] >> 16);
+                    const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&l2)), h = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                    w[t] = dev::e4m3x2(__fmul_rn(l.x, f), __fmul_rn(l.y, f)) | dev::e4m3x2(__fmul_rn(h.x, f), __fmul_rn(h.y, f)) << 16;
+                }
+                reinterpret_cast<uint4 *>(block)[x16] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+}
+
+// The scale that new rows with the largest element `top` make of a block's old one.  (One
+// below 2^-126, which only a cache filled by other means has, is not kept: its reciprocal
+// may be infinite, and a zero's code then NaN.)
+__device__ __forceinline__ float next_scale(float old, float top) {
+    return top <= 448.f * old && (old == 0.f || old >= 0x1p-126f) ? old : fmaxf(e4m3_scale(top), old > 0.f ? 0x1p-126f : 0.f);
+}
+
+// The scale of a block whose row `slot` has an infinity or NaN is a NaN that keeps the
+// scale, a power of two or 0, of the rows before.  They are as they were as soon as that
+// row or one before it is stored again: a rejected token takes no other with it.
+__device__ __forceinline__ float bad_scale(float scale, int slot) { return __uint_as_float(0x7fc00000u | uint32_t(slot) << 8 | __float_as_uint(scale) >> 23); }
+// What an append at row `slot` finds; NaN: rows before it are lost.
+__device__ __forceinline__ float kept_scale(float scale, int slot) {
+    const uint32_t bits = __float_as_uint(scale), e = bits & 0xffu;
+    return scale == scale || (bits & 0xfffff000u) != 0x7fc00000u || e == 0xffu || slot > int(bits >> 8 & 15u) ? scale : __uint_as_float(e << 23);
+}
+
+// What page_rows leaves out: new rows one after the other, where one of them or the
+// block's scale is not finite.
+template <typename T, int VE>
+__device__ __forceinline__ void odd_rows(const RopeArgs &a, int b, int lo, int c, int i0, int n, int j, bool is_v, int lane) {
+    constexpr int U = E4M3_D / (2 * VE);
+    const Unit<T, VE> unit(a, lane % U);
+    const int phys = dev::ld(a.block_table + int64_t(b) * a.max_blocks + (c + i0) / 16);
+    if (phys < 0 || phys >= a.num_blocks) return;  // (recorded)
+    float *sp = (is_v ? a.v_scale : a.k_scale) + int64_t(phys) * a.H_kv + j;
+    uint8_t *block = (is_v ? a.V : a.K) + (int64_t(phys) * a.H_kv + j) * (16 * E4M3_D);
+    const bool rotate = !is_v && unit.turns;
+    float2 x[VE];
+    // row i, rotated, and its largest element; false: it is not stored
+    const auto take = [&](int i, uint32_t &bits) {
+        int place;
+        if (!place_of(a, lo + i, c + i, place)) return false;
+        typename Unit<T, VE>::V raw[2];
+        float cs[VE], sn[VE];
+        unit.load(is_v ? kv_row(a, a.v, a.v_token, b, i, lo + i, j) : kv_row(a, a.k, a.k_token, b, i, lo + i, j), raw);
+        if (rotate) unit.angles(a, place, cs, sn);
+        unit.turn(raw, cs, sn, rotate, x);
+        float most = 0.f;
+        for (int e = 0; e < VE; ++e) most = dev::max_abs_nan(dev::max_abs_nan(most, x[e].x), x[e].y);
+        bits = __reduce_max_sync(FULL, __float_as_uint(most) & 0x7fffffffu);
+        return true;
+    };
+    uint32_t bits;
+    const float first = (c + i0) % 16 > 0 ? dev::ld(sp) : 0.f;
+    bool odd = first != first;
+    for (int i = i0; !odd && i < i0 + n; ++i) odd = take(i, bits) && bits >= 0x7f800000u;
+    for (int i = i0; odd && i < i0 + n; ++i) {
+        const int slot = (c + i) % 16;
+        if (!take(i, bits)) continue;
+        __syncwarp();  // (what the warp has written for the row before)
+        const bool bad = bits >= 0x7f800000u;
+        const float was = slot > 0 ? dev::ld(sp) : 0.f, old = kept_scale(was, slot);
+        const bool lost = old != old;
+        float scale = next_scale(old, bad ? 0.f : __uint_as_float(bits));
+        if (bad && (__float_as_uint(scale) & 0x7fffffu))  // (one that is no power of two has no room)
+            scale = fminf(__uint_as_float((__float_as_uint(scale) & 0x7f800000u) + 0x800000u), 0x1p127f);
+        const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
+        if (slot > 0 && !lost && scale != old) rescale_rows(block, slot, __fmul_rn(old, inv), lane);
+        __syncwarp();
+        if (lane < U)
+            for (int v = 0; v < 2; ++v) {
+                uint32_t codes[VE / 4];
+                for (int t = 0; t < VE / 4; ++t) {
+                    const float2 y = x[v * VE / 2 + 2 * t], z = x[v * VE / 2 + 2 * t + 1];
+                    codes[t] = bad || lost ? 0u : dev::e4m3x2(y.x * inv, y.y * inv) | dev::e4m3x2(z.x * inv, z.y * inv) << 16;
+                }
+                unit.store_codes(block + slot * E4M3_D, v, codes);
+            }
+        if (lane == 0 && !lost) *sp = bad ? bad_scale(scale, slot) : scale;
+        __syncwarp();
+    }
+}
+
+// New rows [i0, i0 + n) of sequence b, all of one block, of KV head j of K or V; true, and
+// nothing stored, where one of them or the block's scale is not finite.
 // The warp holds them as they were read and rotates them twice, for the largest
 // element and for the codes: as fp32 they would take the registers of two warps, and
 // what bounds a prompt is how many reads are in flight.
 template <typename T, int VE>
-__device__ __forceinline__ void page_rows(const RopeArgs &a, int b, int lo, int c, int i0, int n, int j, bool is_v, int lane) {
+__device__ __forceinline__ bool page_rows(const RopeArgs &a, int b, int lo, int c, int i0, int n, int j, bool is_v, int lane) {
     constexpr int U = E4M3_D / (2 * VE), SL = 32 / U, P = 16 / SL;
     const int u = lane % U, slot = lane / U, pos0 = c + i0, s0 = pos0 % 16;
     const Unit<T, VE> unit(a, u);
@@ -290,9 +380,9 @@ __device__ __forceinline__ void page_rows(const RopeArgs &a, int b, int lo, int 
     }
     if (phys < 0 || phys >= a.num_blocks) {
         if (lane == 0) dev::record_error(a.err, ERR_DEVICE_INDEX);
-        return;
+        return false;
     }
-    if (!__any_sync(FULL, live != 0)) return;
+    if (!__any_sync(FULL, live != 0)) return false;
     float *sp = (is_v ? a.v_scale : a.k_scale) + int64_t(phys) * a.H_kv + j;
     const float old = s0 > 0 ? dev::ld(sp) : 0.f;
     uint8_t *block = (is_v ? a.V : a.K) + (int64_t(phys) * a.H_kv + j) * (16 * E4M3_D);
@@ -310,27 +400,12 @@ __device__ __forceinline__ void page_rows(const RopeArgs &a, int b, int lo, int 
         for (int e = 0; e < VE; ++e) most = dev::max_abs_nan(dev::max_abs_nan(most, x[e].x), x[e].y);
     }
     const uint32_t bits = __reduce_max_sync(FULL, __float_as_uint(most) & 0x7fffffffu);  // (infinities and NaN are above all)
-    const bool odd = bits >= 0x7f800000u || old != old;
-    const float top = __uint_as_float(bits);
-    // (a scale below 2^-126, which only a cache filled by other means has, is not kept: its
-    // reciprocal may be infinite, and a zero's code then NaN)
-    const bool fits = top <= 448.f * old && (old == 0.f || old >= 0x1p-126f);
-    const float scale = odd ? __int_as_float(0x7fffffff) : fits ? old : fmaxf(e4m3_scale(top), old > 0.f ? 0x1p-126f : 0.f);
+    if (bits >= 0x7f800000u || old != old) return true;
+    const float scale = next_scale(old, __uint_as_float(bits));
     const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-    if (s0 > 0 && !odd && scale != old) {
+    if (s0 > 0 && scale != old) {
         // the rows before, at the new scale
-        const float f = __fmul_rn(old, inv);
-        for (int x16 = lane; x16 < s0 * (E4M3_D / 16); x16 += 32) {
-            uint4 v = dev::ld(reinterpret_cast<const uint4 *>(block) + x16);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t l2 = dev::e4m3x2_to_f16x2(w[t] & 0xffffu), h2 = dev::e4m3x2_to_f16x2(w[t] >> 16);
-                const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&l2)), h = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                w[t] = dev::e4m3x2(__fmul_rn(l.x, f), __fmul_rn(l.y, f)) | dev::e4m3x2(__fmul_rn(h.x, f), __fmul_rn(h.y, f)) << 16;
-            }
-            reinterpret_cast<uint4 *>(block)[x16] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        rescale_rows(block, s0, __fmul_rn(old, inv), lane);
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) unit.keep(raw[p]);  // (else the compiler holds on to what it has rotated)
@@ -349,21 +424,24 @@ __device__ __forceinline__ void page_rows(const RopeArgs &a, int b, int lo, int 
 #pragma unroll
             for (int t = 0; t < VE / 4; ++t) {
                 const float2 i2 = make_float2(inv, inv), y = dev::mul2(x[v * VE / 2 + 2 * t], i2), z = dev::mul2(x[v * VE / 2 + 2 * t + 1], i2);
-                codes[t] = odd ? 0u : dev::e4m3x2(y.x, y.y) | dev::e4m3x2(z.x, z.y) << 16;
+                codes[t] = dev::e4m3x2(y.x, y.y) | dev::e4m3x2(z.x, z.y) << 16;
             }
             unit.store_codes(row, v, codes);
         }
     }
     if (lane == 0 && (s0 == 0 || scale != old)) *sp = scale;
+    return false;
 }
 
-template <typename T, int VE>
-__device__ __forceinline__ void page_item(const RopeArgs &a, unsigned item, int lane) {
+// ODD: the blocks that are not finite, else the others; are there any of those?
+template <typename T, int VE, bool ODD>
+__device__ __forceinline__ bool page_item(const RopeArgs &a, unsigned item, int lane) {
     // (range, KV head), K and V behind one another; where warps are many, each an item
     const unsigned per = a.both ? a.H_kv : 2 * a.H_kv, range = item / per, w = item - range * per;
     const int j = int(w) < a.H_kv ? int(w) : int(w) - a.H_kv;
     const int t0 = int(range) * a.range, t1 = min(a.total, t0 + a.range);
     // sequence after sequence, those of its blocks whose first new token is in [t0, t1)
+    bool odd = false;
     dev::PackedSeq mine{};
     int b0 = a.cu_seqlens ? 0 : t0 / a.T;  // (without cu_seqlens: the first of the range on)
     for (; b0 < a.B && (a.cu_seqlens || t1 > b0 * a.T); b0 += 32) {
@@ -382,11 +460,23 @@ __device__ __forceinline__ void page_item(const RopeArgs &a, unsigned item, int 
             while (i < n && lo + i < t1) {
                 const int take = min(n - i, 16 - (c + i) % 16);
 #pragma unroll 1
-                for (int v = int(w) >= a.H_kv; v <= (a.both || int(w) >= a.H_kv); ++v) page_rows<T, VE>(a, b0 + src, lo, c, i, take, j, v, lane);
+                for (int v = int(w) >= a.H_kv; v <= (a.both || int(w) >= a.H_kv); ++v) {
+                    if constexpr (ODD)
+                        odd_rows<T, VE>(a, b0 + src, lo, c, i, take, j, v, lane);
+                    else if (page_rows<T, VE>(a, b0 + src, lo, c, i, take, j, v, lane))
+                        odd = true;
+                }
                 i += take;
             }
         }
     }
+    return odd;
+}
+
+// (apart from the others, which would be 3 % slower, single tokens 10 %)
+template <typename T, int VE>
+__device__ __noinline__ void odd_items(const RopeArgs &a, unsigned x, unsigned step, int lane) {
+    for (; x < unsigned(a.page_items); x += step) page_item<T, VE, true>(a, x, lane);
 }
 
 template <typename T, int VE, Mode M>
@@ -400,7 +490,10 @@ __global__ void __launch_bounds__(256, 2) rope_kernel(const __grid_constant__ Ro
     // (loops of their own: in one, each kind of item would have the other's registers spilled)
     const unsigned warp = threadIdx.x >> 5, half = gridDim.x / 2;
     if (M == BLOCKS && (blockIdx.x & 1) == 0) {
-        for (unsigned x = blockIdx.x / 2 * 8 + warp; x < unsigned(a.page_items); x += (gridDim.x - half) * 8) page_item<T, VE>(a, x, lane);
+        const unsigned first = blockIdx.x / 2 * 8 + warp, step = (gridDim.x - half) * 8;
+        bool odd = false;
+        for (unsigned x = first; x < unsigned(a.page_items); x += step) odd |= page_item<T, VE, false>(a, x, lane);
+        if (odd) odd_items<T, VE>(a, first, step, lane);
     } else {
         const unsigned block = M == BLOCKS ? blockIdx.x / 2 : blockIdx.x, blocks = M == BLOCKS ? half : gridDim.x;
         for (unsigned x = block * 8 + warp; x < unsigned(a.total) * a.parts; x += blocks * 8) row_item<T, VE, M>(a, x, lane);
