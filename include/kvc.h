@@ -594,8 +594,8 @@ kvc_status kvc_append_rope(kvc_cache *h, int32_t layer, const kvc_rope *rope, co
  * (off by 2^-12 of itself or 2^-17 of its row's largest).  Otherwise codes are taken as
  * fp16 (exact), query elements too, scaled by a power of two (off by 2^-39 of their row's
  * largest at most).  Either way a probability, times its block's scale of V, is rounded to
- * fp16: off by 2^-11 of itself or by 2^-29 of the largest such product that its row has
- * met, whichever is more.  The softmax's sum takes probabilities as they
+ * fp16: off by 2^-11 of itself or, where more, by 2^-15 / n of the largest such product of
+ * its row (n: the rows that the last token of its block of tokens sees, up to 65,536).  The softmax's sum takes probabilities as they
  * were; fp32 products and sums, one round-to-nearest-even at the end.
  * Limit of one call: 2^30 steps, where a block of floor(r / g) tokens of a sequence
  * (r: 64, or fewer where sequences have fewer query rows per KV head on average; 256

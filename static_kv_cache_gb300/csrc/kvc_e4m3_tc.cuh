@@ -18,8 +18,8 @@
 // the ones before leave, which is exact: four columns, added up at a piece's end with the
 // factors 1, 2^-5, 2^-10 and 2^-15.  With three, 16 times what is left, whatever was 2^-18
 // of a row's first maximum was lost, and with it, beside one key with 97 % of the weight, much of
-// what 16,384 others add up to (the fourth costs 4 %: 32 heads on one KV head 20.9 -> 21.8
-// us, drafts 27.9 -> 29.1).  The tensor cores have the time: they read A for as long as
+// what 16,384 others add up to (the fourth costs 4 %: 32 heads on one KV head 20.9 -> 21.4
+// us, drafts 27.8 -> 28.8).  The tensor cores have the time: they read A for as long as
 // N = 64 takes them.
 //
 // A tile is 128 rows: the blocks of 16 rows of NH KV heads that lie one behind
@@ -45,9 +45,12 @@
 // factor in two steps, as one may be below what fp32 has.)  The
 // references are raised, and the maxima taken at all, only where a P' would pass
 // 2^8: else a tile costs the group one barrier that carries the question.  A reference is
-// set so that the row's largest P' is 2^4: what fp16 rounds away of one is 2^-29 of that at
-// most, and a later score has four bits to go (at 2^0, 2^2, 2^3, 2^4, 2^6: 32 heads on one KV
-// head 21.8, 21.8, 22.3, 22.5, 24.3 us; a batch 33.3, 33.7, 33.6, 34.0, 37.1).
+// set so that the row's largest P' is 2^r.  What fp16 rounds away of one is 2^-(25 + r) of
+// that at most, and a later score has 8 - r bits to go.  r grows with the rows that the
+// segment sees, 0 below 1,024, 4 from 8,192, 6 from 32,768 on, so that all they lose is
+// 2^-15 of the largest: short segments have no time to raise references, long ones hardly
+// notice (r always 0, as it is, always 4: 1,216 sequences of 512 rows 76, 76, 84 us, 32 heads
+// on one KV head 21.4, 22.3, 22.6, a batch 33.0, 33.3, 33.8, long MHA 233).
 //
 // The line of all tiles (sequence after sequence, head group, query rows) is cut
 // into equal shares; a cut segment's pieces go to the workspace as partial results,
@@ -73,7 +76,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int TILE = 128, TILE_BYTES = TILE * E4M3_D, STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int MAX_STAGES = 6;
 constexpr uint32_t TMEM_COLS = 512, S_COL = 0, S_NEXT = 128, O_COL = 256, O_NEXT = 128;  // (a group's)
-constexpr float RESCALE_LOG2 = 8.f, START_LOG2 = 4.f, SMALL_LOG2 = -40.f;
+constexpr float RESCALE_LOG2 = 8.f, SMALL_LOG2 = -40.f;
 constexpr int64_t MAX_LINE = 1 << 30;  // tiles of a call (places are 32-bit numbers)
 constexpr int GROUPS = 2;
 // Softmax warps: two groups of 4, or of 8 where a tile has 16 or 32 query rows per
@@ -784,6 +787,7 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
 #pragma unroll
             for (int r = 0; r < RW; ++r) sum[r] = 0.f;
             const int least = here.c + here.j * a.tt + 1;  // keys that every row of the piece sees
+            const float room = float(min(max(22 - __clz(here.keys), 0), 6));  // log2 of the largest P' where a reference is set
             int i = WIDE || (t0 & 1) == g ? 0 : 1;
             const int first = i;
             for (; i < tiles; i += STEP) {
@@ -885,7 +889,7 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
                         }
                         // (keys that a row sees come before those it does not: one that sees
                         // none in its first tile sees none later)
-                        const float delta = i == first ? (top == -INFINITY ? 0.f : top - START_LOG2) : fmaxf(top - START_LOG2, 0.f);
+                        const float delta = i == first ? (top == -INFINITY ? 0.f : top - room) : fmaxf(top - room, 0.f);
                         corr = ex2(-0.5f * delta);
                         mo = i == first ? delta : mo + delta;
                         sm.neg[g][lane] = -mo;

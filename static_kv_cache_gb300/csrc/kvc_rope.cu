@@ -268,17 +268,17 @@ __device__ __forceinline__ float e4m3_scale(float top) {
 
 // The codes of a block's first rows, times f.
 __device__ __forceinline__ void rescale_rows(uint8_t *block, int rows, float f, int lane) {
-            for (int x16 = lane; x16 < rows * (E4M3_D / 16); x16 += 32) {
-                uint4 v = dev::ld(reinterpret_cast<const uint4 *>(block) + x16);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t l2 = dev::e4m3x2_to_f16x2(w[t] & 0xffffu), h2 = dev::e4m3x2_to_f16x2(w[t] >> 16);
-                    const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&l2)), h = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                    w[t] = dev::e4m3x2(__fmul_rn(l.x, f), __fmul_rn(l.y, f)) | dev::e4m3x2(__fmul_rn(h.x, f), __fmul_rn(h.y, f)) << 16;
-                }
-                reinterpret_cast<uint4 *>(block)[x16] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+    for (int x16 = lane; x16 < rows * (E4M3_D / 16); x16 += 32) {
+        uint4 v = dev::ld(reinterpret_cast<const uint4 *>(block) + x16);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t l2 = dev::e4m3x2_to_f16x2(w[t] & 0xffffu), h2 = dev::e4m3x2_to_f16x2(w[t] >> 16);
+            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&l2)), h = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+            w[t] = dev::e4m3x2(__fmul_rn(l.x, f), __fmul_rn(l.y, f)) | dev::e4m3x2(__fmul_rn(h.x, f), __fmul_rn(h.y, f)) << 16;
+        }
+        reinterpret_cast<uint4 *>(block)[x16] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // The scale that new rows with the largest element `top` make of a block's old one.  (One

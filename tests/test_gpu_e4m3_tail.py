@@ -57,12 +57,24 @@ FORMS = [(1, 1, 1), (8, 2, 1), (32, 8, 1), (8, 2, 3), (32, 1, 1), (64, 1, 1), (1
 @pytest.mark.parametrize("share, rows, where", [(0.9, 32768, "first"), (0.97, 16384, "first"), (0.97, 8192, "middle"), (0.9, 16384, "last"), (0.5, 16384, "flat")])
 @pytest.mark.parametrize("splits", [1, 0])
 def test_sink_and_tail(H, G, n, share, rows, where, splits):
+    _check(H, G, n, share, rows, where, splits, 2.0 ** -29)
+
+
+@pytest.mark.parametrize("H, G, n", FORMS)
+@pytest.mark.parametrize("share, rows", [(0.97, 300), (0.99, 1024), (0.97, 2047), (0.97, 4096)])
+def test_sink_and_short_tail(H, G, n, share, rows):
+    """Fewer rows: the largest probability is 2^0 in those units below 1,024 of them, and all
+    that they lose 2^-15 of it."""
+    _check(H, G, min(n, 60), share, rows, "first", 1, 2.0 ** -15 / rows)
+
+
+def _check(H, G, n, share, rows, where, splits, least):
     """An error of a probability: 2^-11 of it as an fp16 value, with 2^-20 for the exponent (it
-    is below 2^5) and the exponential, or 2^-25 in units in which the largest probability (times scale) that
-    the row meets is 2^4 or more; sums over the keys round once per instruction, of 16
+    is below 2^5) and the exponential, or `least` of the largest probability (times scale) that
+    the row meets, 2^-25 in units in which that is 2^4 or more; sums over the keys round once per instruction, of 16
     keys at least.  The scores are exact."""
     n = min(n, 10) if rows > 20000 else n
-    p = Pool(1, H, G, rows, "fp16" if H != 8 else "bf16", seed=H + n)
+    p = Pool(1, H, G, -(-rows // 16) * 16, "fp16" if H != 8 else "bf16", seed=H + n)
     sink = {"first": 0, "middle": rows // 2 + 5, "last": rows - n, "flat": 3}[where]
     k, v = _fill(p, rows, sink, where == "flat")
     q = _queries(p, n, k, sink, share)
@@ -77,7 +89,7 @@ def test_sink_and_tail(H, G, n, share, rows, where, splits):
     assert float(prob[-1, :, sink].min()) > 0.8 * share
     v = v.repeat_interleave(g, 0)
     ref, mass = torch.einsum("nhj,hjd->nhd", prob, v), torch.einsum("nhj,hjd->nhd", prob, v.abs())
-    err = (2.0 ** -11 + 2.0 ** -20 + (rows / 16 + 8) * 2.0 ** -23) * mass + rows * 2.0 ** -29 * 448 * V_SCALE * prob.amax(2)[..., None]
+    err = (2.0 ** -11 + 2.0 ** -20 + (rows / 16 + 8) * 2.0 ** -23) * mass + rows * least * 448 * V_SCALE * prob.amax(2)[..., None]
     eps = torch.finfo(DT[p.dtype]).eps
     tol = err + eps / 2 * (ref.abs() + err) + (2.0 ** -25 if p.dtype == "fp16" else 0.0)
     worst = ((out.double() - ref).abs() / tol).amax()
