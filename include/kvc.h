@@ -99,13 +99,14 @@ typedef enum {
  * smallest power of two with absmax <= 448 * scale over the block's new rows
  * (not below 2^-126; 0 for zeros); otherwise the scale it had, where the new rows
  * fit it and it is 0 or 2^-126 at least, or else that power of two (2^-126 at least),
- * and the codes of the rows before become e4m3(code * (old scale * (1 / scale))).  A new row with an infinity or NaN makes
- * the block's scale NaN: its rows read as NaN until that row, or one before it, is
- * stored again.  The rows before it are kept in that NaN's last bits, at a scale that is a
- * power of two (what the rule gives, or the next one up), and are there again then; it
- * and the rows behind it in the block are lost.  (Another NaN in a scale's place: until
- * the block's first row is stored again.)  A call's new rows of such a block are stored
- * one by one.  A scale does not shrink before the block's first row is stored again.
+ * and the codes of the rows before become e4m3(code * (old scale * (1 / scale))).  A
+ * scale does not shrink before the block's first row is stored again.  A new row with an
+ * infinity or NaN makes the block's scale NaN: its rows read as NaN until that row, or one
+ * before it, is stored again.  That NaN's last bits keep the scale of the rows before it (a
+ * power of two: what the rule gives, or the next one up), which are there again then; the
+ * bad row and those behind it in the block are lost.  A call's new rows of such a block
+ * are stored one by one.  (Another NaN in a scale's place: until the block's first row is
+ * stored again.)
  * A cache filled by other means may hold any finite scales >= 0, and no NaN codes
  * (0x7f, 0xff) in live rows.  Scales of values below 2^-90 but 0 may be taken as 2^-90;
  * beside scales of values above 2^60, rows whose scale is more than 2^100 smaller may
@@ -591,12 +592,15 @@ kvc_status kvc_append_rope(kvc_cache *h, int32_t layer, const kvc_rope *rope, co
  * sequence are left unwritten.
  * Arithmetic: where sequences have up to 64 query rows per KV head on average, the
  * codes are the tensor cores' operands; a query element is the sum of three e4m3 values
- * (off by 2^-12 of itself or 2^-17 of its row's largest).  Otherwise codes are taken as
- * fp16 (exact), query elements too, scaled by a power of two (off by 2^-39 of their row's
- * largest at most).  Either way a probability, times its block's scale of V, is rounded to
- * fp16: off by 2^-11 of itself or, where more, by 2^-15 / n of the largest such product of
- * its row (n: the rows that the last token of its block of tokens sees, up to 65,536).  The softmax's sum takes probabilities as they
- * were; fp32 products and sums, one round-to-nearest-even at the end.
+ * (off by 2^-12 of itself or 2^-17 of its row's largest), a probability, times its
+ * block's scale of V, that of four (off by 2^-15 of itself or, where more, by 2^-15 / n of
+ * the largest such product of its row; n: the rows that the last token of its block of
+ * tokens sees, up to 65,536).  With more query rows than that, g up to 128 and a block of
+ * 256 of them for each sixth SM, codes are taken as fp16 (exact), query elements too,
+ * scaled by a power of two (off by 2^-39 of their row's largest at most), and
+ * probabilities are rounded to fp16 (2^-11, or 2^-32 of the row's largest).  The average
+ * is over all B sequences, those without tokens among them.  The softmax's sum takes
+ * probabilities as they were; fp32 products and sums, one round-to-nearest-even at the end.
  * Limit of one call: 2^30 steps, where a block of floor(r / g) tokens of a sequence
  * (r: 64, or fewer where sequences have fewer query rows per KV head on average; 256
  * where they have more) takes, per KV head, up to four steps and one for each 128 rows

@@ -115,18 +115,20 @@ kvc_status attend(const kvc_cache *h, int32_t layer, const void *q, const int32_
     while (rows < 64 && rows < tokens * h->group) rows *= 2;
     // Where they are more than 64, the kernel that has query rows on M: it does 256 of
     // them in the time that the other one takes for 80 (16 sequences of 2,048 rows, 32
-    // heads over 8, with 16, 24, 64, 128 tokens: 45, 73, 132, 248 us with the other one,
-    // 58, 59, 71, 111 with it) -- if there is a segment for six SMs at least: the pieces of
+    // heads over 8, with 16, 24, 64, 128 tokens: 48, 79, 143, 269 us with the other one,
+    // 54, 57, 69, 109 with it) -- if there is a segment for six SMs at least: the pieces of
     // fewer are joined in longer than that (8 sequences of 8 tokens over 4,096 rows, 32
-    // heads on one: 30 us with the other one, 46 with it).
+    // heads on one: 32 us with the other one, 46 with it).  The average is over the batch's
+    // slots, as the lengths are on the device: idle slots, and single tokens beside one
+    // long chunk, lower it for the chunk.
     const int g = h->group, pair_tokens = g <= 128 ? 2 * (128 / g) : 0;
     const int64_t seqs = c.batch < total ? c.batch : total;
     const bool many = tokens > 1 && tokens * g > 64 && pair_tokens && (total / pair_tokens + seqs) * c.n_kv_heads * 6 >= h->num_sms;
     // KV heads of a tile: the more, the larger the copies (32 KB of 8 or 4 heads take the
     // time of their bytes, of 2 heads 0.83 us an SM, of one 0.8), but the fewer segments to
     // cut: at least one for five SMs, or their ends, each joined by one CTA, are what the
-    // call waits for (16 sequences of 1,024 - 8,192 rows, 8 heads: 43 us with 8 heads a
-    // tile, 37 with 4, 38.7 with 2; 4 sequences of 64 heads: 237, 238, 270).
+    // call waits for (16 sequences of 1,024 - 8,192 rows, 8 heads: 40 us with 8 heads a
+    // tile, 33.2 with 4, 33.5 with 2, 38 with 1; 4 sequences of 64 heads: 229, 231, 253).
     int nh = 8, map = 3;
     const int64_t row_tiles = cu_seqlens ? (int64_t(total) * h->group + rows - 1) / rows + seqs : seqs;
     while (many ? nh > 1 : (nh > 1 && nh * rows > 32) || c.n_kv_heads % nh || (nh > 1 && row_tiles * (c.n_kv_heads / nh) * 5 < h->num_sms)) nh /= 2, --map;
@@ -137,8 +139,8 @@ kvc_status attend(const kvc_cache *h, int32_t layer, const void *q, const int32_
     if (many) a.gt = 1, a.gg = g, a.tt = pair_tokens;
     a.gg_inverse = (65536 + a.gg - 1) / a.gg;
     // A segment's start and end count as four tiles.  (32 heads on one KV head at 2, 4, 8:
-    // 22.4, 22.0, 21.7 us; drafts 28.1, 28.4, 30.6; with query rows on M, at 2, 3, 4, 6:
-    // prompt chunks 85, 87, 87, 86, a prompt of 4,096 tokens 203, 188, 185, 187.)
+    // 23.7, 22.3, 22.0 us; drafts 31.3, 29.7, 29.2; with query rows on M, at 2, 3, 4, 6:
+    // prompt chunks 84, 87, 87, 86, a prompt of 4,096 tokens 204, 186, 183, 183.)
     a.cost = 4;
     a.groups = c.n_kv_heads / nh;
     a.shift = 7 - map;

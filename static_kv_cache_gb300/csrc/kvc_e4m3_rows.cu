@@ -27,9 +27,9 @@
 // zeros); 9 issues the MMAs.  A cut segment's pieces are joined by the CTA that finds
 // itself the last.  Every wait is bounded, and after one that ran out every role leaves.
 //
-// Measured (bf16, 32 heads over 8): 8 chunks of 512 tokens over 4,096 rows 288 us, 1.01
-// PFLOP/s; a prompt of 4,096 tokens 180 us; 4 chunks of 200 - 500 tokens over up to 4,000
-// rows 84 us (162 with the kernel that has keys on M).  A tile of 256 query rows takes
+// Measured (bf16, 32 heads over 8): 8 chunks of 512 tokens over 4,096 rows 289 us, 1.01
+// PFLOP/s; a prompt of 4,096 tokens 183 us; 4 chunks of 200 - 500 tokens over up to 4,000
+// rows 87 us (190 with the kernel that has keys on M).  A tile of 256 query rows takes
 // 2.3 us, bound by each query tile's chain: 1.2 us its softmax (half of it the maxima),
 // 0.6 its MMAs, the rest hand-overs and the other query tile's MMAs; without the softmax
 // it would take 1.6, without the widening 2.2.  What it took from 162 to 87: codes widened

@@ -13,14 +13,14 @@
 // The other operand has 3 bits of mantissa too, so a query element is taken as the
 // sum of three of them, each what the ones before leave (off by 2^-12, or by 2^-17 of
 // the row's largest): three columns, added up as they are read, or, where a tile has
-// many query rows, three products into one column.  A probability is
-// rounded to fp16 (2^-11; the sum takes it as it is) and split in four, each 32 times what
-// the ones before leave, which is exact: four columns, added up at a piece's end with the
+// many query rows, three products into one column.  A probability is split in
+// four, each 32 times what the ones before leave (off by 2^-15, or by 2^-25 of 1; the
+// softmax's sum takes it as it is): four columns, added up at a piece's end with the
 // factors 1, 2^-5, 2^-10 and 2^-15.  With three, 16 times what is left, whatever was 2^-18
-// of a row's first maximum was lost, and with it, beside one key with 97 % of the weight, much of
-// what 16,384 others add up to (the fourth costs 4 %: 32 heads on one KV head 20.9 -> 21.4
-// us, drafts 27.8 -> 28.8).  The tensor cores have the time: they read A for as long as
-// N = 64 takes them.
+// of a row's first maximum was lost, and with it, beside one key with 97 % of the weight,
+// much of what 16,384 others add up to (the fourth costs 3 %: 32 heads on one KV head 20.9
+// -> 21.4 us, drafts 27.8 -> 28.8).  The tensor cores have the time: they read A for as
+// long as N = 64 takes them.
 //
 // A tile is 128 rows: the blocks of 16 rows of NH KV heads that lie one behind
 // another in the pool, of 8 / NH pages.  One box brings a page's NH heads (NH * 2
@@ -36,21 +36,20 @@
 // thread has one key.  P' is MN-major, so that a thread's probabilities, of all its
 // head's query rows, are neighbouring bytes.  A pair (head, query row) has one
 // reference mo, of the scores with the values' scale in them: P' = 2^(s + log2 vs -
-// mo) stays within the range of the four values (up to 2^8, down to 2^-24, fp16's
-// smallest) whatever the blocks' scales, and P' / vs sums up to what the output is divided
-// by.
+// mo) stays within the range of the four values (up to 2^8, down to 2^-24) whatever the
+// blocks' scales, and P' / vs sums up to what the output is divided by.
 // (Scales of values below 2^-90, zeros among them, count as that in a reference, so
-// that no sum overflows; below 2^-40 the sum has an exponential of its own, as P' may be flushed
-// to zero beside values of common size; and where references differ, sums take the
-// factor in two steps, as one may be below what fp32 has.)  The
-// references are raised, and the maxima taken at all, only where a P' would pass
-// 2^8: else a tile costs the group one barrier that carries the question.  A reference is
-// set so that the row's largest P' is 2^r.  What fp16 rounds away of one is 2^-(25 + r) of
+// that no sum overflows; below 2^-40 the sum has an exponential of its own, as P' may
+// be flushed to zero beside values of common size; and where references differ, sums
+// take the factor in two steps, as one may be below what fp32 has.)  The references
+// are raised, and the maxima taken at all, only where a P' would pass 2^8: else a tile
+// costs the group one barrier that carries the question.  A reference is set so that
+// the row's largest P' is 2^r.  What is cut off below the four values is 2^-(25 + r) of
 // that at most, and a later score has 8 - r bits to go.  r grows with the rows that the
 // segment sees, 0 below 1,024, 4 from 8,192, 6 from 32,768 on, so that all they lose is
-// 2^-15 of the largest: short segments have no time to raise references, long ones hardly
-// notice (r always 0, as it is, always 4: 1,216 sequences of 512 rows 76, 76, 84 us, 32 heads
-// on one KV head 21.4, 22.3, 22.6, a batch 33.0, 33.3, 33.8, long MHA 233).
+// 2^-15 of the largest: short segments have no time to raise references, long ones
+// hardly notice (r always 0, as it is, always 4: 1,216 sequences of 512 rows 76, 76, 84
+// us, 32 heads on one KV head 21.4, 22.3, 22.6, a batch 33.0, 33.3, 33.8, long MHA 233).
 //
 // The line of all tiles (sequence after sequence, head group, query rows) is cut
 // into equal shares; a cut segment's pieces go to the workspace as partial results,
@@ -81,8 +80,10 @@ constexpr int64_t MAX_LINE = 1 << 30;  // tiles of a call (places are 32-bit num
 constexpr int GROUPS = 2;
 // Softmax warps: two groups of 4, or of 8 where a tile has 16 or 32 query rows per
 // head: two warps then share each key, a half of the rows each (the exponents, sums and
-// bytes of 32 rows are more than the registers of one thread, and their latency is its
-// time: prompt chunks 284 -> 262 us, 32 heads on one KV head 25.7 -> 25.0).
+// bytes of 32 rows are more than one thread has registers for; with 16, two warps take
+// what one does or 3 % more where tiles are many, 64 sequences of 4,000 rows with 16 heads
+// on one KV head 25.3 us and 24.9, and less where a call waits for its last pieces, one
+// sequence of 8,048 rows 13.2 us and 14.4).
 // Before them: copies, the issuers of S and O, and, where a tile is of one head, a
 // warp that copies V 16 bytes a lane: 16 boxes of 2 KB a tile take 1.1 us (a box about
 // 50 cycles and five for each of its rows), eight of them beside the warp 0.8.
@@ -91,7 +92,7 @@ struct Warps {
     static constexpr int SOFT0 = ONE ? 4 : 3;
     static constexpr int SPLIT = RT >= 16 ? 2 : 1, RW = RT / SPLIT;  // RW: query rows of a thread
     // The three values of a query element: columns of one product (whose latency is that
-    // of four instructions, not twelve: one user 9.5 -> 8.8 us) or three products.
+    // of four instructions, not twelve: one user 8.4 us and 8.7) or three products.
     static constexpr bool COLUMNS = RT <= 4;
     static constexpr int SETS = GROUPS * SPLIT, NSOFT = 4 * SETS, THREADS = 32 * (SOFT0 + NSOFT);
 };
@@ -485,15 +486,20 @@ __device__ __forceinline__ void join(const E4m3TcArgs &a, int64_t out_row, int f
     }
 }
 
-// An fp16 pair's four e4m3 values each, the next 32 times what the ones before leave:
-// exact up to 2^8.  A value leaves at most 2^-4 of what it is of, 8 of 2^8, so the next
-// is 2^8 at most too; three take 12 bits of fp16's 11, and the fourth's last step, 2^-9 *
-// 2^-15, is fp16's smallest number.
-__device__ __forceinline__ void split4(uint32_t h, uint32_t (&c)[4]) {
+// Two numbers up to 2^8 as four e4m3 values each, the next 32 times what the ones before
+// leave.  A value leaves at most 2^-4 of what it is of, 8 of 2^8, so the next is 2^8 at
+// most too.  What the first leaves is rounded to fp16 (2^-15 of the number), whose 11 bits the
+// other three hold, but for what is below half of the last one's smallest step, 2^-25.
+// (The number itself rounded to fp16 first: 2^-11 of it, the error against 64 bits with
+// fp16 queries a fifth larger, and at most 2 % in time, 32 query rows a tile.)
+__device__ __forceinline__ void split4(float2 f, uint32_t (&c)[4]) {
     const __half2 minus = __float2half2_rn(-32.f), times = __float2half2_rn(32.f);
-    __half2 x = *reinterpret_cast<const __half2 *>(&h);
+    c[0] = dev::e4m3x2(f.x, f.y);
+    const uint32_t b0 = dev::e4m3x2_to_f16x2(c[0]);
+    const float2 r = dev::fma2(__half22float2(*reinterpret_cast<const __half2 *>(&b0)), make_float2(-32.f, -32.f), dev::mul2(f, make_float2(32.f, 32.f)));
+    __half2 x = __floats2half2_rn(r.x, r.y);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 1; k < 4; ++k) {
         uint16_t r;
         asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
         c[k] = r;
@@ -953,9 +959,8 @@ __global__ void __launch_bounds__(Warps<RT, ONE>::THREADS, 1) e4m3_attn_kernel(c
                         } else {
                             sum[0] = fmaf(f.x, per, sum[0]);
                         }
-                        const __half2 h = __floats2half2_rn(f.x, f.y);
                         uint32_t two[4];
-                        split4(*reinterpret_cast<const uint32_t *>(&h), two);
+                        split4(f, two);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) c[k][e / 4] = e % 4 ? __byte_perm(c[k][e / 4], two[k], 0x5410) : two[k];
                     }

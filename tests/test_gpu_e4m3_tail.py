@@ -69,8 +69,8 @@ def test_sink_and_short_tail(H, G, n, share, rows):
 
 
 def _check(H, G, n, share, rows, where, splits, least):
-    """An error of a probability: 2^-11 of it as an fp16 value, with 2^-20 for the exponent (it
-    is below 2^5) and the exponential, or `least` of the largest probability (times scale) that
+    """An error of a probability: 2^-15 of it as four e4m3 values (2^-11 as an fp16 value, with
+    query rows on M), with 2^-20 for the exponent (it is below 2^5) and the exponential, or `least` of the largest probability (times scale) that
     the row meets, 2^-25 in units in which that is 2^4 or more; sums over the keys round once per instruction, of 16
     keys at least.  The scores are exact."""
     n = min(n, 10) if rows > 20000 else n
@@ -89,7 +89,7 @@ def _check(H, G, n, share, rows, where, splits, least):
     assert float(prob[-1, :, sink].min()) > 0.8 * share
     v = v.repeat_interleave(g, 0)
     ref, mass = torch.einsum("nhj,hjd->nhd", prob, v), torch.einsum("nhj,hjd->nhd", prob, v.abs())
-    err = (2.0 ** -11 + 2.0 ** -20 + (rows / 16 + 8) * 2.0 ** -23) * mass + rows * least * 448 * V_SCALE * prob.amax(2)[..., None]
+    err = ((2.0 ** -11 if n == 200 else 2.0 ** -15) + 2.0 ** -20 + (rows / 16 + 8) * 2.0 ** -23) * mass + rows * least * 448 * V_SCALE * prob.amax(2)[..., None]
     eps = torch.finfo(DT[p.dtype]).eps
     tol = err + eps / 2 * (ref.abs() + err) + (2.0 ** -25 if p.dtype == "fp16" else 0.0)
     worst = ((out.double() - ref).abs() / tol).amax()
