@@ -563,6 +563,9 @@ typedef struct {
  *   k_out        device, [total, H_kv, d_h], or NULL: the rotated keys as well,
  *                for kvc_prompt_attn (may be k itself where that is dense, but
  *                not on a KVC_E4M3 handle)
+ *                Otherwise q_out and k_out must not overlap each other or the
+ *                inputs, from their first token's elements to their last's
+ *                (KVC_ERR_INVALID)
  * Paged handles: rows whose table entry is outside [0, num_blocks) are not stored
  * and KVC_ERR_DEVICE_INDEX is recorded.
  * Host errors: KVC_ERR_INVALID (also where the handle's device is not current),

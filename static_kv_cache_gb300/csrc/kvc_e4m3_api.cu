@@ -14,6 +14,11 @@ using kvc::device_current;
 
 int row_bytes_of(const kvc_cache *h) { return h->row_dtype == KVC_FP32 ? 4 : 2; }
 
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a_bytes > 0 && b_bytes > 0 && (x < y ? y - x < uintptr_t(a_bytes) : x - y < uintptr_t(b_bytes));
+}
+
 // What every append fills in alike.
 kvc::RopeArgs rope_args(const kvc_cache *h, int32_t layer) {
     const kvc_config &c = h->cfg;
@@ -73,8 +78,8 @@ kvc_status refusal(const kvc_cache *h, const void *q, const void *out, int32_t t
     const int64_t rows = int64_t(total) * h->cfg.n_heads;
     if (rows > 0x7fffffff) return KVC_ERR_UNSUPPORTED;
     // (a row's pieces are several CTAs', which read its queries)
-    const uintptr_t bytes = uintptr_t(rows) * kvc::E4M3_D * row_bytes_of(h), a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(out);
-    return (a < b ? b - a : a - b) < bytes ? KVC_ERR_INVALID : KVC_OK;
+    const int64_t bytes = rows * kvc::E4M3_D * row_bytes_of(h);
+    return overlap(q, bytes, out, bytes) ? KVC_ERR_INVALID : KVC_OK;
 }
 
 kvc_status attend(const kvc_cache *h, int32_t layer, const void *q, const int32_t *cu_seqlens, const int32_t *cache_index,
@@ -279,6 +284,12 @@ kvc_status kvc_append_rope(kvc_cache *h, int32_t layer, const kvc_rope *rope, co
         return KVC_ERR_ALIGNMENT;
     if (k_stride * eb % 16 || v_stride * eb % 16 || (q && q_stride * eb % 16)) return KVC_ERR_ALIGNMENT;
     if ((q && q_out == q && q_stride != q_row) || (k_out == k && k_stride != kv_row)) return KVC_ERR_INVALID;  // (over rows not read yet)
+    const auto bytes = [&](int64_t stride, int64_t row) { return ((total - 1) * stride + row) * eb; };
+    const int64_t qn = q ? bytes(q_stride, q_row) : 0, kn = bytes(k_stride, kv_row), vn = bytes(v_stride, kv_row);
+    const int64_t qon = q ? bytes(q_row, q_row) : 0, kon = k_out ? bytes(kv_row, kv_row) : 0;
+    if ((q_out != q && overlap(q_out, qon, q, qn)) || overlap(q_out, qon, k, kn) || overlap(q_out, qon, v, vn) || overlap(q_out, qon, k_out, kon) ||
+        (k_out != k && overlap(k_out, kon, k, kn)) || overlap(k_out, kon, q, qn) || overlap(k_out, kon, v, vn))
+        return KVC_ERR_INVALID;
     kvc::RopeArgs a = rope_args(h, layer);
     a.q = static_cast<const uint8_t *>(q);
     a.k = static_cast<const uint8_t *>(k);

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from tests import _rows
 from tests._e4m3 import D, Pool, ints
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +29,31 @@ def test_refused_attention_calls():
     y[:2] = q
     kvc.check(kvc.kvc_decode_step(p.h, 0, y, k, v, valid, 0, y[2:]))
     assert y[2:].any() and torch.equal(y[:2], q) and p.error() == 0 and p.intact()
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_rope_outputs_over_other_inputs(cache):
+    """Warps write outputs while others still read: refused, but for q and k in their own place."""
+    p = Pool(2, 4, 2, 64) if cache == "e4m3" else _rows.Cache("bf16", 1, 2, 4, 2, D, 64)
+    kvc = p.kvc
+    K = p.K.clone()
+    buf = torch.zeros(64 * D, dtype=torch.bfloat16, device="cuda")
+    q, k, v, out, far = (buf.data_ptr() + 2 * D * x for x in (0, 12, 18, 24, 36))  # 3 tokens: 12, 6, 6 rows; outputs 12, 6
+    fused = buf.data_ptr() + 2 * D * 40                                         # 3 tokens of 4 + 2 + 2 rows
+    c, cu, row = ints([5, 0]), ints([0, 1, 3]), 2 * D
+
+    def call(q_out, k_out, q=q, k=k, v=v, qs=4, ks=2, vs=2):
+        return kvc.kvc_append_rope(p.h, 0, None, q, qs * D, k, ks * D, v, vs * D, cu, c, 3, q_out, k_out)
+    for q_out, k_out in ((k, None), (v, None), (q + row, None), (k - 11 * row, None), (v + 5 * row, None), (out, out), (out, out + 11 * row),
+                         (out, v), (out, q), (out, q + 11 * row), (out, k + row), (out, v + 5 * row)):
+        assert call(q_out, k_out) == kvc.KVC_ERR_INVALID, (q_out, k_out)
+    for at in (0, 4, 6, 23):
+        assert call(fused + at * row, None, fused, fused + 4 * row, fused + 6 * row, 8, 8, 8) == kvc.KVC_ERR_INVALID
+        assert call(out, fused + at * row, fused, fused + 4 * row, fused + 6 * row, 8, 8, 8) == kvc.KVC_ERR_INVALID
+    view = torch.int16 if cache == "bf16" else torch.uint8
+    assert torch.equal(p.K.view(view), K.view(view)) and not buf.any()
+    for q_out, k_out in ((out, None), (out, far), (q, None), (q, far)):  # side by side, and q in its place
+        kvc.check(call(q_out, k_out))
+    assert call(q, k) == (kvc.KVC_ERR_INVALID if cache == "e4m3" else kvc.KVC_OK)
+    kvc.check(kvc.kvc_append_rope(p.h, 0, None, None, 0, k, 2 * D, v, 2 * D, cu, c, 3, None, far))
+    assert p.error() == 0 and p.intact()
