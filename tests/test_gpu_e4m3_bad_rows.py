@@ -86,3 +86,57 @@ def test_rows_behind_a_bad_one_are_lost():
     assert store(x[:2], 5) == (False, False)
     assert store(x[:1], 0) == (True, True)
     assert p.error() == 0 and p.intact()
+
+
+@pytest.mark.parametrize("G, n", [(8, (1503, 1300)), (2, (70, 33))])
+def test_bad_rows_in_prompts(G, n):
+    """Blocks of long and short prompts, rotated: bad rows in some of them, the others as ever."""
+    p = Pool(2, G, G, 1600, seed=G)
+    cached = (37, 16)
+    p.fill(cached)
+    state, kvc, total = p.host(), p.kvc, sum(n)
+    x = p.normal(total, 3 * G, D, tag="qkv")
+    rng = np.random.default_rng(G)
+    for r in rng.integers(0, total, 12):
+        x[int(r), int(rng.integers(G, 3 * G)), int(rng.integers(D))] = float(rng.choice([np.inf, -np.inf, np.nan]))
+    a = rng.uniform(-40, 40, (1600, 32))
+    cs = np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)
+    csd, q_out = torch.from_numpy(cs).cuda(), torch.zeros(total, G, D, dtype=torch.bfloat16, device="cuda")
+    rope = kvc.make_rope(csd, 1600, 64, True)
+    flat, s = x.view(total, -1), 3 * G * D
+    kvc.check(kvc.kvc_append_rope(p.h, 0, rope, flat, s, flat[:, G * D:], s, flat[:, 2 * G * D:], s, ints([0, n[0], total]), ints(cached), total, q_out, None))
+    host = x.float().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        k = e4m3.rotate(host[:, G:2 * G], cs, [c + i for c, m in zip(cached, n) for i in range(m)], 64, True)
+    for b, lo, hi in ((0, 0, n[0]), (1, n[0], total)):
+        e4m3.append(state[0], state[1], p.order[b], cached[b], k[lo:hi])
+        e4m3.append(state[2], state[3], p.order[b], cached[b], host[lo:hi, 2 * G:])
+    _same_bits(p, state)
+    assert np.isnan(state[1]).any() and np.isnan(state[3]).any()
+    assert p.error() == 0 and p.intact()
+
+
+def test_bad_rows_in_dense_appends():
+    """kvc_append's layout, and kvc_decode_step: a token's bad row, then the token again."""
+    p = Pool(3, 4, 2, 96, "fp16", seed=11)
+    kvc, cached = p.kvc, [20, 0, 7]
+    p.fill(cached)
+    state = p.host()
+    k, v = p.normal(3, 2, 40, D, tag="k"), p.normal(3, 2, 40, D, tag="v")
+    k[0, 1, 7, 3], v[2, 0, 39, 0], v[1, 1, 0, 5] = np.nan, np.inf, -np.inf
+    kvc.check(kvc.kvc_append(p.h, 0, k, v, ints(cached), 40))
+    for b, c in enumerate(cached):
+        for i, y in ((0, k), (2, v)):
+            e4m3.append(state[i], state[i + 1], p.order[b], c, y[b].transpose(0, 1).float().cpu().numpy())
+    _same_bits(p, state)
+    # sequence 2's last token again, through the step; the others on from rows that are good
+    at = [26, 0, 46]
+    k1, v1, q = p.normal(3, 2, 1, D, tag="k1"), p.normal(3, 2, 1, D, tag="v1"), p.normal(3, 4, D, tag="q")
+    out = torch.zeros_like(q)
+    kvc.check(kvc.kvc_decode_step(p.h, 0, q, k1, v1, ints([a + 1 for a in at]), 0, out))
+    for b, c in enumerate(at):
+        for i, y in ((0, k1), (2, v1)):
+            e4m3.append(state[i], state[i + 1], p.order[b], c, y[b].transpose(0, 1).float().cpu().numpy())
+    _same_bits(p, state)
+    check_attention(p, q, out, [0, 1, 2, 3], at)
+    assert p.error() == 0 and p.intact()
